@@ -70,7 +70,11 @@ typedef enum {
     CCA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed          */
     CCA_ERR_TIMEOUT = 5,     /* a bounded device-side wait ran out         */
     CCA_ERR_RANGE = 6,       /* a value beyond the fp16 range was clamped  */
-    CCA_ERR_SCRATCH = 7      /* request exceeds the library's fixed scratch */
+    CCA_ERR_SCRATCH = 7,     /* request exceeds the library's fixed scratch */
+    CCA_ERR_SEQLENS = 8,     /* packed sequence offsets that do not ascend
+                                within the packed rows                      */
+    CCA_ERR_PAGE = 9         /* a page table entry, row number or parent
+                                outside the paged cache                     */
 } cca_status;
 
 /* Element type of an output that may be written in either precision. */
@@ -361,11 +365,191 @@ cca_status cca_lca_cache_append(cca_cache *c, float *q_sum, const void *q_t, con
                                 const void *v_t, int d_rope, cudaStream_t stream);
 
 /*
+ * Packed prompts: S sequences of different lengths, one behind the other,
+ * without padding (sections 全局感知池化, 局部保留模块 and
+ * 全局-局部模块可微融合 for a whole sequence, each by itself).
+ * cu [S + 1] (int32, device memory, 4-byte aligned): sequence s is rows
+ * cu[s] .. cu[s + 1] - 1; 0 <= cu[0], ascending (equal neighbours are an
+ * empty sequence), cu[S] <= total.  Offsets that break this make the calls
+ * write nothing and are reported by cca_device_status (CCA_ERR_SEQLENS).
+ * Rows that no sequence owns (before cu[0], behind cu[S]) are never read
+ * into a result, whatever they hold, and their outputs stay as they were.
+ * 1 <= S <= CCA_MAX_SEQS.
+ *
+ * A packed tensor is `heads` x `total` rows of d contiguous elements; row t
+ * of head h starts head * h + row * t elements behind `data`.  Both memory
+ * orders that occur are so described: [heads, total, d] and
+ * [total, heads, d], with or without gaps.  data: 16-byte aligned; row and
+ * head: at least d and multiples of 8 (the stride of an extent of 1 is not
+ * read).  For outputs: 32-byte aligned, multiples of 16, and rows that do
+ * not overlap.
+ */
+typedef struct {
+    void *data;
+    int64_t row, head; /* strides in elements */
+} cca_rows;
+
+#define CCA_MAX_SEQS 8192
+
+/*
+ * cca_pool for packed prompts: Q [Hq], K, V [Hkv] packed bf16 tensors.
+ * Kc, Vc (fp16, written): contiguous [Hkv, total / g, d]; the core row of
+ * group j of sequence s is row cu[s] / g + j (division rounding down), so
+ * that sequences never share a row; rows that hold no group become zero.
+ */
+cca_status cca_pool_packed(const cca_rows *Q, const cca_rows *K, const cca_rows *V,
+                           const int32_t *cu, void *Kc, void *Vc, int S, int Hq, int Hkv,
+                           int64_t total, int d, int g, cudaStream_t stream);
+
+/* Bytes of device workspace cca_attn_prefill_packed needs (0 for an invalid
+ * shape): the order in which it takes the sequences' query blocks. */
+size_t cca_packed_workspace_bytes(int S, int64_t total);
+
+/*
+ * cca_attn_prefill for packed prompts: O [Hq] (o_dtype) gets each
+ * sequence's causal attention over its own core rows (Kc, Vc from
+ * cca_pool_packed) and its own window.  w >= total is plain causal
+ * attention: no core row is seen, Kc and Vc may be NULL.
+ * workspace: cca_packed_workspace_bytes(S, total) bytes, 256-byte aligned;
+ * its contents need no initialisation.  Calls sharing a workspace must not
+ * overlap on the GPU.
+ */
+cca_status cca_attn_prefill_packed(const cca_rows *Q, const cca_rows *K, const cca_rows *V,
+                                   const void *Kc, const void *Vc, const int32_t *cu,
+                                   const cca_rows *O, cca_dtype o_dtype, int S, int Hq, int Hkv,
+                                   int64_t total, int d, int g, int w, void *workspace,
+                                   size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Paged decode cache: the cache of section 基于 Triton 的底层加速 (core rows
+ * of completed groups, raw rows of the window) for B rows of any lengths
+ * that share their memory in pages.  A page holds `page` rows of every
+ * key/value head; core rows and raw rows have a pool each, the same for
+ * every layer of a model (page p of each layer's pool belongs to the same
+ * tokens):
+ *   k_core, v_core: fp16 [layers, core_pages, Hkv, page, d]
+ *   k_raw, v_raw:   bf16 [layers, raw_pages, Hkv, page, d]
+ * Row b holds lens[b] tokens (0: the row is free).  Its core row j is row
+ * j % page of page core_table[b, j / page], its token p is row p % page of
+ * page raw_table[b, p / page].  An entry is -1 where the row has no page:
+ * behind its end, and in raw_table before the window of its newest token.
+ * core_ref[p], raw_ref[p] count the entries that name page p; a page of
+ * count 0 is free.  A full page may belong to several rows
+ * (cca_paged_fork); the page a row writes next is its own.
+ * page: a power of two, 16 .. 1024.  Hq / Hkv <= 16.  B <= 4096.
+ * core_cols and core_pages may both be 0: a cache of plain causal
+ * attention, for w >= raw_cols * page (no window ever ends).
+ * The buffers belong to the caller; lens is 8-byte, pools 16-byte aligned.
+ * A new cache: tables filled with -1, counts and lens with 0.
+ *
+ * The calls below read lens and tables on the device: a sequence of them can
+ * be captured in a CUDA graph.  Their workspace (cca_paged_workspace_bytes
+ * bytes, 256-byte aligned) is zero-filled once before its first use with a
+ * cache, and every call leaves it ready for the next; calls sharing a
+ * workspace must not overlap on the GPU.
+ */
+typedef struct {
+    void *k_core, *v_core, *k_raw, *v_raw;
+    int32_t *core_table, *raw_table; /* [B, core_cols], [B, raw_cols] */
+    int32_t *core_ref, *raw_ref;     /* [core_pages], [raw_pages] */
+    long long *lens;                 /* [B] */
+    int layers, B, Hq, Hkv, d, g, w, page;
+    int core_cols, raw_cols, core_pages, raw_pages;
+} cca_paged_cache;
+
+size_t cca_paged_workspace_bytes(const cca_paged_cache *c);
+
+/*
+ * Room for more tokens: row b is lengthened by n_new[b] >= 0 tokens
+ * (device memory, B entries; NULL: by n, every row that is not free), as
+ * prompt or as the next token of a step, for all layers at once.  lens[b]
+ * grows and the row gets the pages that the longer row needs: raw pages
+ * for the window of its new last token and everything behind, core pages
+ * for its complete groups.  The free pages of lowest number are taken, rows
+ * in order, a row's columns in order; then the raw pages that lie wholly
+ * before the new window are given back.  The new tokens' contents are
+ * written by cca_paged_fill or cca_paged_step.  A row that does not fit (its
+ * table's columns; or the pages that it and the rows before it need exceed
+ * the free ones of a pool) keeps its length and pages and is reported by
+ * cca_device_status (CCA_ERR_CAPACITY).
+ */
+cca_status cca_paged_reserve(const cca_paged_cache *c, const long long *n_new, long long n,
+                             cudaStream_t stream);
+
+/*
+ * Fill one layer's pages from packed prompts: sequence s becomes row
+ * rows[s] (int32, device memory) of the cache, which cca_paged_reserve has
+ * given the length of the sequence.  K, V: packed bf16 tensors [Hkv]; Kc,
+ * Vc: their core rows from cca_pool_packed (NULL for a cache without core
+ * pages).  Copied are the rows of the last token's window and the core rows
+ * of all complete groups.  A sequence whose row is out of range, not of its
+ * length, or named by a later sequence too is left out; so are token and
+ * core rows whose page is missing or belongs to another row as well.  Both
+ * are reported (CCA_ERR_PAGE).
+ */
+cca_status cca_paged_fill(const cca_paged_cache *c, int layer, const cca_rows *K,
+                          const cca_rows *V, const void *Kc, const void *Vc, const int32_t *cu,
+                          const int32_t *rows, int S, int64_t total, cudaStream_t stream);
+
+/*
+ * Attention of the newest token t = lens[b] - 1 of every row over one
+ * layer of the cache: q_t [B, Hq, d] (bf16) -> o_t [B, Hq, d] (o_dtype).
+ * A free row gets a zero output; so does a row longer than its table, which
+ * is reported (CCA_ERR_CAPACITY).  Keys whose page is missing are left out
+ * and reported (CCA_ERR_PAGE).
+ */
+cca_status cca_attn_decode_paged(const cca_paged_cache *c, int layer, const void *q_t, void *o_t,
+                                 cca_dtype o_dtype, void *workspace, size_t workspace_bytes,
+                                 cudaStream_t stream);
+
+/*
+ * One decode step of one layer in one launch: writes the newest token t =
+ * lens[b] - 1 of every row (k_t, v_t [B, Hkv, d], for which
+ * cca_paged_reserve has made room) to its page, pools the group it completes
+ * into its core row, and computes cca_attn_decode_paged of it.  lens is not
+ * changed, so that the layers of a model take their steps one after the
+ * other.  (A row that cca_paged_reserve refused still ends in the token
+ * before: its step writes that one again.)  A token or core row whose page
+ * is missing or belongs to another row as well is not written, and is
+ * reported (CCA_ERR_PAGE).
+ */
+cca_status cca_paged_step(const cca_paged_cache *c, int layer, const void *q_t, const void *k_t,
+                          const void *v_t, void *o_t, cca_dtype o_dtype, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Rows take over other rows: afterwards row b holds what row parent[b]
+ * (int32, device memory, B entries) held before the call; parent[b] = b
+ * keeps a row, -1 frees it.  One call so forks a prompt into several samples,
+ * reorders the beams of a search and frees finished rows, for all layers.
+ * Full pages are shared; a partly filled last page (raw or core) stays with
+ * the parent itself if it keeps its row, else with the lowest row that
+ * takes it over, and the others get a copy in the free page of lowest number
+ * (rows in order, pages freed by this call included).  A row for
+ * whose copies no page is left is freed and reported (CCA_ERR_CAPACITY).  A
+ * parent out of range keeps its row and is reported (CCA_ERR_PAGE).
+ */
+cca_status cca_paged_fork(const cca_paged_cache *c, const int32_t *parent, void *workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Compact the pools: the pages in use of the highest numbers move, for all
+ * layers, to the free ones of the lowest numbers (both in ascending order),
+ * until the pages in use are 0 .. live - 1; tables and counts follow.
+ * live [2] (device memory, 8-byte aligned, written): pages in use of the
+ * core and of the raw pool, to which the pools can be cut.
+ */
+cca_status cca_paged_compact(const cca_paged_cache *c, long long *live, void *workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Synchronise `stream`, then report CCA_ERR_CUDA if a CUDA error is
  * pending, CCA_ERR_TIMEOUT if any kernel of this library recorded a
  * timed-out wait since the last call, CCA_ERR_CAPACITY if a per-row call
- * met a row longer than its cache, CCA_ERR_RANGE if one clamped a value to
- * the fp16 range, else CCA_OK.  The records are cleared.
+ * met a row longer than its cache or a paged cache had no page for a row,
+ * CCA_ERR_PAGE or CCA_ERR_SEQLENS if a call met such data in device memory,
+ * CCA_ERR_RANGE if one clamped a value to the fp16 range, else CCA_OK.  The
+ * records are cleared.
  */
 cca_status cca_device_status(cudaStream_t stream);
 

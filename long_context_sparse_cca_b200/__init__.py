@@ -17,9 +17,14 @@ Entry points (same names as the C ABI):
     cca_cache_append_rows, cca_attn_decode_rows (per-row lengths in device
     memory), cca_lca_pool, cca_lca_cache_prefill, cca_lca_cache_append (the
     LCA variant's condensation; ``lca_query_sums`` allocates the running
-    query sums its cache calls keep), cca_selftest_wait_timeout,
-    cca_device_status
-and the ``Cache`` class holding a decode cache's device buffers.
+    query sums its cache calls keep), cca_pool_packed,
+    cca_packed_workspace_bytes, cca_attn_prefill_packed (prompts of different
+    lengths without padding), cca_paged_workspace_bytes, cca_paged_reserve,
+    cca_paged_fill, cca_attn_decode_paged, cca_paged_step, cca_paged_fork,
+    cca_paged_compact (a decode cache whose rows share memory in pages),
+    cca_selftest_wait_timeout, cca_device_status
+and the ``Cache`` and ``PagedCache`` classes holding a decode cache's device
+buffers.
 """
 
 from __future__ import annotations
@@ -39,6 +44,8 @@ CCA_ERR_CUDA = 4
 CCA_ERR_TIMEOUT = 5
 CCA_ERR_RANGE = 6
 CCA_ERR_SCRATCH = 7
+CCA_ERR_SEQLENS = 8
+CCA_ERR_PAGE = 9
 CCA_BF16 = 0
 CCA_F32 = 1
 NOALLOC_SCRATCH_BYTES = 4 << 20  # CCA_NOALLOC_SCRATCH_BYTES of include/cca.h
@@ -50,7 +57,10 @@ EXPORTS = ("cca_pool", "cca_attn_prefill", "cca_cache_prefill",
            "cca_attn_decode_noalloc", "cca_selftest_wait_timeout",
            "cca_cache_append_rows", "cca_attn_decode_rows", "cca_decode_step",
            "cca_attn_prefill_lse", "cca_attn_backward", "cca_attn_backward_workspace_bytes",
-           "cca_lca_pool", "cca_lca_cache_prefill", "cca_lca_cache_append")
+           "cca_lca_pool", "cca_lca_cache_prefill", "cca_lca_cache_append",
+           "cca_pool_packed", "cca_packed_workspace_bytes", "cca_attn_prefill_packed",
+           "cca_paged_workspace_bytes", "cca_paged_reserve", "cca_paged_fill",
+           "cca_attn_decode_paged", "cca_paged_step", "cca_paged_fork", "cca_paged_compact")
 
 
 class CCAError(RuntimeError):
@@ -68,6 +78,19 @@ class _CacheStruct(ctypes.Structure):
                 ("d", ctypes.c_int), ("g", ctypes.c_int), ("w", ctypes.c_int),
                 ("core_cap", ctypes.c_int64), ("tail_cap", ctypes.c_int64),
                 ("len", ctypes.c_int64)]
+
+
+class _RowsStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
+class _PagedStruct(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in
+                 ("k_core", "v_core", "k_raw", "v_raw", "core_table", "raw_table", "core_ref",
+                  "raw_ref", "lens")] +
+                [(n, ctypes.c_int) for n in
+                 ("layers", "B", "Hq", "Hkv", "d", "g", "w", "page", "core_cols", "raw_cols",
+                  "core_pages", "raw_pages")])
 
 
 _lib = None
@@ -118,6 +141,28 @@ def lib():
     L.cca_cache_append_rows.restype = st
     L.cca_attn_decode_rows.argtypes = [CP, P, P, P, i, P, ctypes.c_size_t, P]
     L.cca_attn_decode_rows.restype = st
+    RP, PP, sz = ctypes.POINTER(_RowsStruct), ctypes.POINTER(_PagedStruct), ctypes.c_size_t
+    L.cca_pool_packed.argtypes = [RP, RP, RP, P, P, P, i, i, i, i64, i, i, P]
+    L.cca_pool_packed.restype = st
+    L.cca_packed_workspace_bytes.argtypes = [i, i64]
+    L.cca_packed_workspace_bytes.restype = sz
+    L.cca_attn_prefill_packed.argtypes = [RP, RP, RP, P, P, P, RP, i, i, i, i, i64, i, i, i,
+                                          P, sz, P]
+    L.cca_attn_prefill_packed.restype = st
+    L.cca_paged_workspace_bytes.argtypes = [PP]
+    L.cca_paged_workspace_bytes.restype = sz
+    L.cca_paged_reserve.argtypes = [PP, P, ctypes.c_longlong, P]
+    L.cca_paged_reserve.restype = st
+    L.cca_paged_fill.argtypes = [PP, i, RP, RP, P, P, P, P, i, i64, P]
+    L.cca_paged_fill.restype = st
+    L.cca_attn_decode_paged.argtypes = [PP, i, P, P, i, P, sz, P]
+    L.cca_attn_decode_paged.restype = st
+    L.cca_paged_step.argtypes = [PP, i, P, P, P, P, i, P, sz, P]
+    L.cca_paged_step.restype = st
+    L.cca_paged_fork.argtypes = [PP, P, P, sz, P]
+    L.cca_paged_fork.restype = st
+    L.cca_paged_compact.argtypes = [PP, P, P, sz, P]
+    L.cca_paged_compact.restype = st
     L.cca_selftest_wait_timeout.argtypes = [ctypes.c_uint, P]
     L.cca_selftest_wait_timeout.restype = st
     L.cca_device_status.argtypes = [P]
@@ -533,6 +578,330 @@ def cca_attn_decode_noalloc(cache: Cache, q_t, o_t=None, out_dtype=None, stream=
         ctypes.byref(cache.struct), _dev(q_t, "q_t"), _dev(o_t, "o_t", o_t.dtype), od,
         _stream(stream)), "cca_attn_decode_noalloc")
     return o_t
+
+
+# ---- packed prompts: sequences of different lengths without padding
+
+def _here(t, name: str):
+    """``t`` is a CUDA tensor of the current device (the library launches
+    on that one)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != _torch().cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return t
+
+
+def _tensor(t, name: str, shape, dtype):
+    """Pointer of a contiguous tensor of this shape on the current device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    return ctypes.c_void_p(_here(t, name).data_ptr())
+
+
+def _rows(t, name: str, shape, dtype=None):
+    """A [heads, total, d] tensor of any row and head strides as the
+    library's packed tensor."""
+    want = dtype or _torch().bfloat16
+    if t.dtype != want or t.shape != shape:
+        raise ValueError(f"{name} must be a {want} tensor {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    head, row, one = t.stride()
+    if one != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return _RowsStruct(_here(t, name).data_ptr(), row, head)
+
+
+def _offsets(cu, name: str = "cu"):
+    if cu.dtype != _torch().int32 or cu.dim() != 1 or cu.numel() < 2 or not cu.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of S + 1 offsets")
+    return ctypes.c_void_p(_here(cu, name).data_ptr())
+
+
+def _packed_shapes(Q, K):
+    if Q.dim() != 3 or K.dim() != 3:
+        raise ValueError("Q, K and V must be [heads, total, d]")
+    Hq, total, d = Q.shape
+    return Hq, K.shape[0], total, d
+
+
+def cca_pool_packed(Q, K, V, cu, g: int, Kc=None, Vc=None, stream=None):
+    """cca_pool for packed prompts: Q [Hq,total,d], K/V [Hkv,total,d] (bf16,
+    rows of any stride: views of [total,heads,d] included), sequence s in
+    rows cu[s] .. cu[s + 1] - 1 (cu: int32, CUDA, [S + 1]).
+
+    Returns (Kc, Vc) [Hkv, total // g, d] fp16; the groups of sequence s
+    start at row cu[s] // g, rows without a group are zero.
+    """
+    torch = _torch()
+    Hq, Hkv, total, d = _packed_shapes(Q, K)
+    shape = (Hkv, total // int(g) if g > 0 else 0, d)
+    if Kc is None:
+        Kc = torch.empty(shape, dtype=torch.float16, device=Q.device)
+    if Vc is None:
+        Vc = torch.empty(shape, dtype=torch.float16, device=Q.device)
+    _check(lib().cca_pool_packed(
+        _rows(Q, "Q", (Hq, total, d)), _rows(K, "K", (Hkv, total, d)),
+        _rows(V, "V", (Hkv, total, d)), _offsets(cu), _tensor(Kc, "Kc", shape, torch.float16),
+        _tensor(Vc, "Vc", shape, torch.float16), cu.numel() - 1, Hq, Hkv, total, d, int(g),
+        _stream(stream)), "cca_pool_packed")
+    return Kc, Vc
+
+
+def cca_packed_workspace_bytes(S: int, total: int) -> int:
+    return int(lib().cca_packed_workspace_bytes(int(S), int(total)))
+
+
+def cca_attn_prefill_packed(Q, K, V, Kc, Vc, cu, g: int, w: int, O=None, out_dtype=None,
+                            workspace=None, stream=None):
+    """cca_attn_prefill for packed prompts (cca_pool_packed gives the
+    layout, Kc and Vc).  w >= total is plain causal attention: Kc and Vc may
+    then be None.  Returns O [Hq, total, d] in ``out_dtype`` (bf16 default,
+    or fp32), in Q's memory order when allocated here; rows that belong to
+    no sequence are not written.
+    """
+    torch = _torch()
+    Hq, Hkv, total, d = _packed_shapes(Q, K)
+    S = cu.numel() - 1
+    if O is None:
+        dt = torch.bfloat16 if out_dtype is None else out_dtype
+        if Q.stride(0) < Q.stride(1):  # [total, Hq, d] in memory
+            O = torch.empty((total, Hq, d), dtype=dt, device=Q.device).transpose(0, 1)
+        else:
+            O = torch.empty((Hq, total, d), dtype=dt, device=Q.device)
+    if workspace is None:
+        workspace = torch.empty(max(cca_packed_workspace_bytes(S, total), 256),
+                                dtype=torch.uint8, device=Q.device)
+        if stream is not None:  # freed on return: not before the work on that stream is done
+            workspace.record_stream(stream)
+    core = (Hkv, total // int(g) if g > 0 else 0, d)
+    _check(lib().cca_attn_prefill_packed(
+        _rows(Q, "Q", (Hq, total, d)), _rows(K, "K", (Hkv, total, d)),
+        _rows(V, "V", (Hkv, total, d)),
+        None if Kc is None else _tensor(Kc, "Kc", core, torch.float16),
+        None if Vc is None else _tensor(Vc, "Vc", core, torch.float16), _offsets(cu),
+        _rows(O, "O", (Hq, total, d), O.dtype), _odtype(O.dtype), S, Hq, Hkv, total, d, int(g),
+        int(w), ctypes.c_void_p(_here(workspace, "workspace").data_ptr()), workspace.numel(),
+        _stream(stream)), "cca_attn_prefill_packed")
+    return O
+
+
+# ---- the paged decode cache
+
+class PagedCache:
+    """A decode cache for B rows of any lengths that share their memory in
+    pages of ``page`` rows: core rows (fp16) in ``core_pages`` pages, raw
+    rows (bf16) in ``raw_pages`` pages, the same page numbers in every one of
+    ``layers`` layers.  ``max_len``: the longest row the tables take.
+    core_pages = 0 gives a cache of plain causal attention.
+
+    ``lens`` (int64 [B]), ``core_table`` and ``raw_table`` (int32 [B, cols],
+    -1: no page), ``core_ref`` and ``raw_ref`` (int32, table entries per
+    page) are views of one tensor, ``tables``; ``pools`` holds k_core,
+    v_core, k_raw, v_raw [layers, pages, Hkv, page, d].
+    """
+
+    def __init__(self, B: int, Hq: int, Hkv: int, d: int, g: int, w: int, page: int,
+                 core_pages: int, raw_pages: int, max_len: int, layers: int = 1, device="cuda"):
+        torch = _torch()
+        if min(B, Hkv, d, g, page, raw_pages, max_len, layers) < 1 or core_pages < 0:
+            raise ValueError("sizes of a PagedCache must be positive")
+        core_cols = max(-(-(max_len // g) // page), 1) if core_pages else 0
+        kh = dict(dtype=torch.float16, device=device)
+        kw = dict(dtype=torch.bfloat16, device=device)
+        pools = (torch.zeros((layers, core_pages, Hkv, page, d), **kh),
+                 torch.zeros((layers, core_pages, Hkv, page, d), **kh),
+                 torch.zeros((layers, raw_pages, Hkv, page, d), **kw),
+                 torch.zeros((layers, raw_pages, Hkv, page, d), **kw))
+        self._set(B, core_cols, -(-max_len // page), pools, Hq, g, w)
+        for t in (self.lens, self.core_ref, self.raw_ref):
+            t.zero_()
+        self.core_table.fill_(-1)
+        self.raw_table.fill_(-1)
+
+    def _set(self, B, core_cols, raw_cols, pools, Hq, g, w):
+        torch = _torch()
+        self.pools = pools
+        self.k_core, self.v_core, self.k_raw, self.v_raw = pools
+        layers, core_pages, Hkv, page, d = self.k_core.shape
+        raw_pages = self.k_raw.shape[1]
+        device = self.k_raw.device
+        n = (2 * B, B * core_cols, B * raw_cols, core_pages, raw_pages)
+        self.tables = torch.empty(sum(n), dtype=torch.int32, device=device)
+        parts = self.tables.split(n)
+        self.lens = parts[0].view(torch.int64)
+        self.core_table = parts[1].view(B, core_cols)
+        self.raw_table = parts[2].view(B, raw_cols)
+        self.core_ref, self.raw_ref = parts[3], parts[4]
+        self.struct = _PagedStruct(
+            *(t.data_ptr() for t in (*pools, self.core_table, self.raw_table, self.core_ref,
+                                     self.raw_ref, self.lens)),
+            layers, B, int(Hq), Hkv, d, int(g), int(w), page, core_cols, raw_cols, core_pages,
+            raw_pages)
+        # zero-filled once, as the library asks for
+        self.workspace = torch.zeros(max(cca_paged_workspace_bytes(self), 256),
+                                     dtype=torch.uint8, device=device)
+
+    @classmethod
+    def from_tensors(cls, core_table, raw_table, core_ref, raw_ref, lens, k_core, v_core, k_raw,
+                     v_raw, Hq: int, g: int, w: int) -> "PagedCache":
+        """A cache over the given pools (kept, not copied) with a copy of the
+        given tables, counts and lengths."""
+        torch = _torch()
+        B = lens.numel()
+        for name, t, dt, shape in (
+                ("core_table", core_table, torch.int32, (B, core_table.shape[-1])),
+                ("raw_table", raw_table, torch.int32, (B, raw_table.shape[-1])),
+                ("core_ref", core_ref, torch.int32, k_core.shape[1:2]),
+                ("raw_ref", raw_ref, torch.int32, k_raw.shape[1:2]),
+                ("lens", lens, torch.int64, (B,)),
+                ("k_core", k_core, torch.float16, k_core.shape),
+                ("v_core", v_core, torch.float16, k_core.shape),
+                ("k_raw", k_raw, torch.bfloat16, k_raw.shape),
+                ("v_raw", v_raw, torch.bfloat16, k_raw.shape)):
+            if t.dtype != dt or t.shape != shape or not t.is_contiguous() or \
+                    t.device != k_raw.device:
+                raise ValueError(f"{name} must be a contiguous {dt} tensor {tuple(shape)} on "
+                                 f"{k_raw.device}")
+        if k_core.dim() != 5 or k_raw.dim() != 5 or k_core.shape[:1] != k_raw.shape[:1] or \
+                k_core.shape[2:] != k_raw.shape[2:]:
+            raise ValueError("pools must be [layers, pages, Hkv, page, d]")
+        c = object.__new__(cls)
+        c._set(B, core_table.shape[1], raw_table.shape[1], (k_core, v_core, k_raw, v_raw), Hq, g, w)
+        for mine, given in ((c.lens, lens), (c.core_table, core_table), (c.raw_table, raw_table),
+                            (c.core_ref, core_ref), (c.raw_ref, raw_ref)):
+            mine.copy_(given)
+        return c
+
+    def state_dict(self) -> dict:
+        """Host copy of the cache, for saving and later restoring a session."""
+        st = self.struct
+        return {"shape": {n: int(getattr(st, n)) for n in ("Hq", "g", "w")},
+                **{n: getattr(self, n).to("cpu", copy=True) for n in self._TENSORS}}
+
+    @classmethod
+    def from_state_dict(cls, state: dict, device="cuda") -> "PagedCache":
+        """A cache on ``device`` holding what ``state_dict`` saved."""
+        return cls.from_tensors(*(state[n].to(device, copy=True) for n in cls._TENSORS), **state["shape"])
+
+    _TENSORS = ("core_table", "raw_table", "core_ref", "raw_ref", "lens", "k_core", "v_core",
+                "k_raw", "v_raw")
+
+    def __getattr__(self, name):
+        if name in ("layers", "B", "Hq", "Hkv", "d", "g", "w", "page", "core_cols", "raw_cols",
+                    "core_pages", "raw_pages"):
+            return getattr(self.struct, name)
+        raise AttributeError(name)
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (*self.pools, self.tables))
+
+
+def cca_paged_workspace_bytes(cache: PagedCache) -> int:
+    return int(lib().cca_paged_workspace_bytes(ctypes.byref(cache.struct)))
+
+
+def _paged(cache: PagedCache):
+    """The cache's struct, once its buffers are known to be on the current
+    device."""
+    _here(cache.tables, "cache")
+    return ctypes.byref(cache.struct)
+
+
+def _paged_workspace(cache: PagedCache, workspace):
+    ws = cache.workspace if workspace is None else _here(workspace, "workspace")
+    return ctypes.c_void_p(ws.data_ptr()), ws.numel()
+
+
+def cca_paged_reserve(cache: PagedCache, n, stream=None) -> None:
+    """Lengthen rows and give them the pages of their new tokens: ``n`` is a
+    number of tokens for every row that is not free, or an int64 CUDA tensor
+    [B] of each row's.  Raw pages before the new window are given back."""
+    torch = _torch()
+    if isinstance(n, torch.Tensor):
+        each, n = _tensor(n, "n", (cache.B,), torch.int64), 0
+    else:
+        each = None
+    _check(lib().cca_paged_reserve(_paged(cache), each, int(n), _stream(stream)),
+           "cca_paged_reserve")
+
+
+def cca_paged_fill(cache: PagedCache, K, V, Kc, Vc, cu, rows, layer: int = 0,
+                   stream=None) -> None:
+    """Fill one layer's pages from packed prompts K/V [Hkv,total,d] with
+    their core rows Kc/Vc (cca_pool_packed; None without core pages):
+    sequence s becomes row rows[s] (int32, CUDA, [S]), which
+    cca_paged_reserve has given the sequence's length."""
+    torch = _torch()
+    total = K.shape[1]
+    S = cu.numel() - 1
+    core = (cache.Hkv, total // cache.g, cache.d)
+    _check(lib().cca_paged_fill(
+        _paged(cache), int(layer), _rows(K, "K", (cache.Hkv, total, cache.d)),
+        _rows(V, "V", (cache.Hkv, total, cache.d)),
+        None if Kc is None else _tensor(Kc, "Kc", core, torch.float16),
+        None if Vc is None else _tensor(Vc, "Vc", core, torch.float16), _offsets(cu),
+        _tensor(rows, "rows", (S,), torch.int32), S, total, _stream(stream)), "cca_paged_fill")
+
+
+def cca_attn_decode_paged(cache: PagedCache, q_t, layer: int = 0, o_t=None, out_dtype=None,
+                          workspace=None, stream=None):
+    """Attention of the newest token of every row: q_t [B,Hq,d] -> o_t
+    [B,Hq,d]; free rows get zeros.  Capturable in a CUDA graph."""
+    torch = _torch()
+    shape = (cache.B, cache.Hq, cache.d)
+    if o_t is None:
+        o_t = torch.empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+                          device=q_t.device)
+    _check(lib().cca_attn_decode_paged(
+        _paged(cache), int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16),
+        _tensor(o_t, "o_t", shape, o_t.dtype), _odtype(o_t.dtype),
+        *_paged_workspace(cache, workspace), _stream(stream)), "cca_attn_decode_paged")
+    return o_t
+
+
+def cca_paged_step(cache: PagedCache, q_t, k_t, v_t, layer: int = 0, o_t=None, out_dtype=None,
+                   workspace=None, stream=None):
+    """One decode step of one layer in one launch: append the newest token of
+    every row (q_t [B,Hq,d], k_t/v_t [B,Hkv,d]; cca_paged_reserve(cache, 1)
+    has made room for it, once for all layers) and return its attention
+    output o_t [B,Hq,d].  Capturable in a CUDA graph."""
+    torch = _torch()
+    shape, kv = (cache.B, cache.Hq, cache.d), (cache.B, cache.Hkv, cache.d)
+    if o_t is None:
+        o_t = torch.empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype,
+                          device=q_t.device)
+    _check(lib().cca_paged_step(
+        _paged(cache), int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16),
+        _tensor(k_t, "k_t", kv, torch.bfloat16), _tensor(v_t, "v_t", kv, torch.bfloat16),
+        _tensor(o_t, "o_t", shape, o_t.dtype), _odtype(o_t.dtype),
+        *_paged_workspace(cache, workspace), _stream(stream)), "cca_paged_step")
+    return o_t
+
+
+def cca_paged_fork(cache: PagedCache, parent, workspace=None, stream=None) -> None:
+    """Row b becomes what row parent[b] was (int32, CUDA, [B]; b: keeps it,
+    -1: frees it), for all layers.  Full pages are shared, partly filled last
+    ones copied: samples of one prompt, beams that change places, rows that
+    are done."""
+    torch = _torch()
+    _check(lib().cca_paged_fork(
+        _paged(cache), _tensor(parent, "parent", (cache.B,), torch.int32),
+        *_paged_workspace(cache, workspace), _stream(stream)), "cca_paged_fork")
+
+
+def cca_paged_compact(cache: PagedCache, live=None, workspace=None, stream=None):
+    """Move the pages in use to the front of their pools, for all layers.
+    Returns ``live`` (int64, CUDA, [2]): pages in use of the core and of the
+    raw pool."""
+    torch = _torch()
+    if live is None:
+        live = torch.empty(2, dtype=torch.int64, device=cache.tables.device)
+    _check(lib().cca_paged_compact(
+        _paged(cache), _tensor(live, "live", (2,), torch.int64),
+        *_paged_workspace(cache, workspace), _stream(stream)), "cca_paged_compact")
+    return live
 
 
 def cca_selftest_wait_timeout(limit_us: int = 1000, stream=None) -> None:

@@ -62,6 +62,8 @@ constexpr float kF16Max = 65504.0f;
 constexpr unsigned int kStatusTimeout = 1u;  // a bounded wait ran out
 constexpr unsigned int kStatusRange = 2u;    // a value exceeded the fp16 range
 constexpr unsigned int kStatusCapacity = 4u; // a row's length exceeded the cache
+constexpr unsigned int kStatusSeqlens = 8u;  // packed offsets out of order or range
+constexpr unsigned int kStatusPage = 16u;    // a page or row number outside the cache
 
 __device__ __forceinline__ float clamp_f16(float x, bool &over)
 {

@@ -66,6 +66,26 @@ cudaError_t launch_prefill(const void *Q, const void *K, const void *V,
                            int B, int Hq, int Hkv, int64_t T, int d, int g,
                            int w, cudaStream_t s, float *lse = nullptr);
 
+// Packed sequences: one packed tensor (element strides of a row and of a
+// head), the list of their 256-row query blocks (most key tiles first), and
+// the calls of the packed prompts.
+struct PackedRows {
+    void *data;
+    int64_t row, head;
+};
+inline int64_t packed_max_blocks(int S, int64_t total) { return total / 256 + S; }
+cudaError_t launch_packed_plan(const int *cu, int S, int64_t total, int g, int4 *blocks,
+                               int *count, cudaStream_t s);
+size_t pool_packed_smem(int S, int r, int g);
+cudaError_t launch_prefill_packed(const PackedRows &Q, const PackedRows &K, const PackedRows &V,
+                                  const void *Kc, const void *Vc, const PackedRows &O, bool o_f32,
+                                  const int *cu, int S, int Hq, int Hkv, int64_t total, int d,
+                                  int g, int w, void *workspace, cudaStream_t s);
+cudaError_t launch_pool_packed(const PackedRows &Q, const PackedRows &K, const PackedRows &V,
+                               const int *cu, void *Kc, void *Vc, int S, int Hq, int Hkv,
+                               int64_t total, int d, int g, cudaStream_t s);
+cudaError_t packed_status_read_clear(unsigned int *v);
+
 // Backward pass (training).  Workspace layout (byte offsets, 256-aligned):
 // fp16 copies of Q and dO, D = rowsum(dO * O), fp32 dKc and dVc.
 struct BwLayoutHost {

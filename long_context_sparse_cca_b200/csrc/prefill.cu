@@ -87,6 +87,11 @@ struct Params {
     void *O;
     int o_f32;
     float *lse;  // [B, Hq, T]: log2 of each row's softmax denominator (LSE instance)
+    // packed sequences (PK instance): the query blocks in the order in which
+    // they are taken, and the output's strides
+    const int4 *blocks;     // {first row, rows, block, first core row} of its sequence
+    const int *block_count;
+    int64_t o_row, o_head;
 };
 
 __device__ __forceinline__ int ws_of(int t, int g, int w)
@@ -97,16 +102,50 @@ __device__ __forceinline__ int ws_of(int t, int g, int w)
 
 // Geometry of one 256-row block.
 struct Geom {
+    int row0, core0;           // PK: first row and first core row of the sequence
+    int T;                     // rows of the sequence
     int b, hq, h, t0, tlast;
     int ws_lo;                 // ws(t0): first local key
     int n_local, n_core_tiles, n_tiles;
 };
 
+__device__ __forceinline__ void geom_tiles(Geom &G, int blk, const Params &p)
+{
+    G.t0 = blk * 256;
+    G.tlast = min(G.t0 + 255, G.T - 1);
+    G.ws_lo = ws_of(G.t0, p.g, p.w);
+    const int nc_hi = ws_of(G.tlast, p.g, p.w) / p.g;
+    G.n_core_tiles = (nc_hi + 127) / 128;
+    G.n_local = (G.tlast - G.ws_lo + 1 + 127) / 128;
+    G.n_tiles = G.n_local + G.n_core_tiles;
+}
+
 // HM: head-major item order (all blocks of a head before the next head).
-template <bool HM>
-__device__ __forceinline__ Geom geom(int item, const Params &p)
+// PK: the blocks of packed sequences, from the list (most key tiles first).
+template <bool HM, bool PK>
+__device__ __forceinline__ Geom geom(int item, int n_blocks, const Params &p)
 {
     Geom G;
+    if constexpr (PK) {
+        int i;
+        if constexpr (HM) {
+            G.hq = item / n_blocks;
+            i = item - G.hq * n_blocks;
+        } else {
+            i = item / p.Hq;
+            G.hq = item - i * p.Hq;
+        }
+        const int4 e = __ldg(p.blocks + i);
+        G.row0 = e.x;
+        G.T = e.y;
+        G.core0 = e.w;
+        G.b = 0;
+        G.h = G.hq / p.r;
+        geom_tiles(G, e.z, p);
+        return G;
+    }
+    G.row0 = G.core0 = 0;
+    G.T = p.T;
     const int bhq_count = p.B * p.Hq;
     // Latest blocks (most core tiles) first.  Across heads when the core
     // rows of all heads fit in L2, so that concurrent items have equal
@@ -124,13 +163,7 @@ __device__ __forceinline__ Geom geom(int item, const Params &p)
     G.b = bhq / p.Hq;
     G.hq = bhq - G.b * p.Hq;
     G.h = G.hq / p.r;
-    G.t0 = blk * 256;
-    G.tlast = min(G.t0 + 255, p.T - 1);
-    G.ws_lo = ws_of(G.t0, p.g, p.w);
-    const int nc_hi = ws_of(G.tlast, p.g, p.w) / p.g;
-    G.n_core_tiles = (nc_hi + 127) / 128;
-    G.n_local = (G.tlast - G.ws_lo + 1 + 127) / 128;
-    G.n_tiles = G.n_local + G.n_core_tiles;
+    geom_tiles(G, blk, p);
     return G;
 }
 
@@ -233,7 +266,12 @@ __device__ __forceinline__ float row_max128(const float (&x)[128])
 // 2^(logit / ln 2) over the row's keys), which the backward kernels need;
 // a separate instance, so that the inference kernel is unchanged.
 // HM: item order (geom), a separate instance for the same reason.
-template <int D, bool LSE, bool HM>
+// PK: packed sequences, likewise.  A tile's rows behind the end of its
+// sequence are other sequences' rows or belong to none: their scores are
+// masked by position like every other key's, and their value rows, which
+// P V would multiply by zero weights (0 x NaN = NaN), are set to zero in
+// shared memory.
+template <int D, bool LSE, bool HM, bool PK>
 __global__ void __launch_bounds__(352, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ,
                    const __grid_constant__ CUtensorMap tmK,
@@ -292,26 +330,28 @@ __global__ void __launch_bounds__(352, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = bars->tmem_base;
+    const int n_blocks = PK ? __ldg(p.block_count) : p.n_blocks;
+    const int n_items = PK ? n_blocks * p.Hq : p.n_items;
 
     if (warp == 8) {
         // ------------------------------------------------ TMA producer
         if (lane == 0) {
             uint32_t kc = 0, vc = 0, qc = 0;
             bool ok = true;
-            for (int item = blockIdx.x; ok && item < p.n_items; item += gridDim.x) {
-                const Geom G = geom<HM>(item, p);
+            for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
+                const Geom G = geom<HM, PK>(item, n_blocks, p);
                 if (qc > 0 && !(ok = lane_wait(&bars->q_empty, (qc - 1) & 1, bars))) break;
                 mbar_arrive_expect_tx(&bars->q_full, 2 * C::TILE_BYTES);
                 for (int hh = 0; hh < 2; ++hh)
                     for (int bx = 0; bx < C::NBOX; ++bx)
                         tma_load_3d(sQ + hh * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ,
-                                    &bars->q_full, bx * 64, G.t0 + hh * 128,
+                                    &bars->q_full, bx * 64, G.row0 + G.t0 + hh * 128,
                                     G.b * p.Hq + G.hq);
                 ++qc;
                 const int z = G.b * p.Hkv + G.h;
                 for (int j = 0; j < G.n_tiles; ++j) {
                     const bool core = tile_is_core(G, j);
-                    const int key0 = tile_key0(G, j);
+                    const int key0 = tile_key0(G, j) + (core ? G.core0 : G.row0);
                     const CUtensorMap *mk = core ? &tmKc : &tmK;
                     const CUtensorMap *mv = core ? &tmVc : &tmV;
                     {
@@ -384,9 +424,9 @@ __global__ void __launch_bounds__(352, 1)
                         mma_ss(d_tmem, a0 + off, b0 + off, idesc, kk > 0 ? 1u : 0u);
                     }
                 };
-                for (int item = blockIdx.x; ok && item < p.n_items;
+                for (int item = blockIdx.x; ok && item < n_items;
                      item += gridDim.x, ++k) {
-                    const Geom G = geom<HM>(item, p);
+                    const Geom G = geom<HM, PK>(item, n_blocks, p);
                     if (!(ok = lane_wait(&bars->q_full, k & 1, bars))) break;
                     for (int j = 0; ok && j < G.n_tiles; ++j, ++it) {
                         const bool core = tile_is_core(G, j);
@@ -430,9 +470,9 @@ __global__ void __launch_bounds__(352, 1)
                         mma_ts(d_tmem, a_tmem + kk * 8, b0 + kk * 128, idesc,
                                (first && kk == 0) ? 0u : 1u);
                 };
-                for (int item = blockIdx.x; ok && item < p.n_items;
+                for (int item = blockIdx.x; ok && item < n_items;
                      item += gridDim.x, ++k) {
-                    const Geom G = geom<HM>(item, p);
+                    const Geom G = geom<HM, PK>(item, n_blocks, p);
                     for (int j = 0; ok && j < G.n_tiles; ++j, ++it) {
                         const bool core = tile_is_core(G, j);
                         const uint32_t sv = vc % C::VST;
@@ -468,8 +508,8 @@ __global__ void __launch_bounds__(352, 1)
         const uint32_t o_addr = tmem + lane_off + C::O_COL + hh * D;
         uint32_t it = 0;  // key tiles over all items
         bool ok = true;
-        for (int item = blockIdx.x; ok && item < p.n_items; item += gridDim.x) {
-            const Geom G = geom<HM>(item, p);
+        for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
+            const Geom G = geom<HM, PK>(item, n_blocks, p);
             const bool core_block = G.n_core_tiles > 0;
             const int t0h = G.t0 + hh * 128;       // first row of this half
             const int t = t0h + row;
@@ -559,6 +599,23 @@ __global__ void __launch_bounds__(352, 1)
                     }
                 }
                 tmem_wait_st();
+                if (PK && hh == 0) {
+                    // value rows behind the sequence's end (see above): half
+                    // A's P V is issued first and waits for these warps
+                    const int last = core ? G.T / p.g - 1 : G.T - 1;
+                    if (key0 + 127 > last) {
+                        const uint32_t sv = it % C::VST;
+                        if (!(ok = warp_wait(&bars->v_full[sv], (it / C::VST) & 1, bars))) break;
+                        if (key0 + row > last) {
+#pragma unroll
+                            for (int c = 0; c < C::NBOX * 8; ++c)
+                                *reinterpret_cast<uint4 *>(sV + sv * C::TILE_BYTES +
+                                                           (c >> 3) * C::BOX_BYTES + row * 128 +
+                                                           (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            fence_proxy_async_smem();
+                        }
+                    }
+                }
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->p_full[hh]);
@@ -574,10 +631,13 @@ __global__ void __launch_bounds__(352, 1)
                     for (int c = row; c < C::TILE_BYTES / 16; c += 128) {
                         const uint4 v = q4[c];
                         uint4 h;
+                        const bool before = over;
                         h.x = pack_f16x2(clamp_f16(bf16_lo(v.x), over), clamp_f16(bf16_hi(v.x), over));
                         h.y = pack_f16x2(clamp_f16(bf16_lo(v.y), over), clamp_f16(bf16_hi(v.y), over));
                         h.z = pack_f16x2(clamp_f16(bf16_lo(v.z), over), clamp_f16(bf16_hi(v.z), over));
                         h.w = pack_f16x2(clamp_f16(bf16_lo(v.w), over), clamp_f16(bf16_hi(v.w), over));
+                        // a query row behind the sequence's end is not reported
+                        if (PK && t0h + ((c >> 3) & 127) >= G.T) over = before;
                         q4[c] = h;
                     }
                     if (over) atomicOr(&g_prefill_status, kStatusRange);
@@ -595,7 +655,9 @@ __global__ void __launch_bounds__(352, 1)
             // before its tensor memory is released
             const float inv = 1.0f / l_run;
             const int64_t orow = (static_cast<int64_t>(G.b) * p.Hq + G.hq) * p.T + t;
-            const bool store = t < p.T;
+            const bool store = t < G.T;
+            const int64_t oelem =
+                PK ? G.hq * p.o_head + (static_cast<int64_t>(G.row0) + t) * p.o_row : orow * D;
             if (LSE && store) p.lse[orow] = (m_run == -INFINITY ? 0.f : m_run) + __log2f(l_run);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -609,7 +671,7 @@ __global__ void __launch_bounds__(352, 1)
                 if (!store) continue;
                 if (p.o_f32) {
                     float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.O) +
-                                                             orow * D + c * 32);
+                                                             oelem + c * 32);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         dst[q] = make_float4(o[4 * q] * inv, o[4 * q + 1] * inv,
@@ -618,7 +680,7 @@ __global__ void __launch_bounds__(352, 1)
                     // 32-byte stores: each thread writes its own row, so a
                     // store fills whole sectors (measured on B200: 3-4%
                     // faster at 128K context than 16-byte stores)
-                    uint16_t *dst = static_cast<uint16_t *>(p.O) + orow * D + c * 32;
+                    uint16_t *dst = static_cast<uint16_t *>(p.O) + oelem + c * 32;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         uint32_t w[8];
@@ -678,6 +740,9 @@ cudaError_t launch_d(const void *Q, const void *K, const void *V, const void *Kc
     p.O = O;
     p.o_f32 = o_f32 ? 1 : 0;
     p.lse = lse;
+    p.blocks = nullptr;
+    p.block_count = nullptr;
+    p.o_row = p.o_head = 0;
     int dev = 0, sms = 148, l2 = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -686,8 +751,64 @@ cudaError_t launch_d(const void *Q, const void *K, const void *V, const void *Kc
     // head-major when the core keys and values of all heads (fp16) exceed
     // half the L2
     const bool hm = 4.0 * static_cast<double>(B) * Hkv * m * D > 0.5 * static_cast<double>(l2);
-    auto kern = lse ? (hm ? prefill_kernel<D, true, true> : prefill_kernel<D, true, false>)
-                    : (hm ? prefill_kernel<D, false, true> : prefill_kernel<D, false, false>);
+    auto kern = lse ? (hm ? prefill_kernel<D, true, true, false> : prefill_kernel<D, true, false, false>)
+                    : (hm ? prefill_kernel<D, false, true, false> : prefill_kernel<D, false, false, false>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         C::SMEM);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, C::THREADS, C::SMEM, s>>>(mQ, mK, mV, mKc, mVc, p);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_packed_d(const PackedRows &Q, const PackedRows &K, const PackedRows &V,
+                            const void *Kc, const void *Vc, const PackedRows &O, bool o_f32,
+                            const int4 *blocks, const int *block_count, int64_t max_blocks, int Hq,
+                            int Hkv, int64_t total, int g, int w, cudaStream_t s)
+{
+    using C = Pf<D>;
+    CUtensorMap mQ, mK, mV, mKc, mVc;
+    const int64_t m = total / g;
+    bool ok = make_map(&mQ, Q.data, D, total, Hq, false, Q.row, Q.head) &&
+              make_map(&mK, K.data, D, total, Hkv, false, K.row, K.head) &&
+              make_map(&mV, V.data, D, total, Hkv, false, V.row, V.head);
+    if (Kc != nullptr && m > 0)
+        ok = ok && make_map(&mKc, Kc, D, m, Hkv, true) && make_map(&mVc, Vc, D, m, Hkv, true);
+    else {  // no core rows: the core maps are never read
+        mKc = mK;
+        mVc = mV;
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    Params p;
+    p.B = 1;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.r = Hq / Hkv;
+    p.T = 0;
+    p.g = g;
+    p.w = w;
+    p.m = 0;
+    p.n_blocks = p.n_items = 0;
+    p.scale_log2 = kLog2e / sqrtf(static_cast<float>(D));
+    p.O = O.data;
+    p.o_f32 = o_f32 ? 1 : 0;
+    p.lse = nullptr;
+    p.blocks = blocks;
+    p.block_count = block_count;
+    p.o_row = O.row;
+    p.o_head = O.head;
+    int dev = 0, sms = 148, l2 = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev);
+    const int64_t most = max_blocks * Hq;
+    const int grid = static_cast<int>(most < sms ? most : sms);
+    // head by head, as above, when what a query may look far back into (the
+    // core rows; for plain causal attention all keys and values) exceeds
+    // half the L2
+    const int64_t far_rows = w >= total ? total : m;
+    const bool hm = 4.0 * static_cast<double>(Hkv) * far_rows * D > 0.5 * static_cast<double>(l2);
+    auto kern = hm ? prefill_kernel<D, false, true, true> : prefill_kernel<D, false, false, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          C::SMEM);
     if (e != cudaSuccess) return e;
@@ -696,6 +817,23 @@ cudaError_t launch_d(const void *Q, const void *K, const void *V, const void *Kc
 }
 
 }  // namespace
+
+cudaError_t launch_prefill_packed(const PackedRows &Q, const PackedRows &K, const PackedRows &V,
+                                  const void *Kc, const void *Vc, const PackedRows &O, bool o_f32,
+                                  const int *cu, int S, int Hq, int Hkv, int64_t total, int d,
+                                  int g, int w, void *workspace, cudaStream_t s)
+{
+    int *count = static_cast<int *>(workspace);
+    int4 *blocks = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + 256);
+    const cudaError_t e = launch_packed_plan(cu, S, total, g, blocks, count, s);
+    if (e != cudaSuccess) return e;
+    const int64_t most = packed_max_blocks(S, total);
+    if (d == 128)
+        return launch_packed_d<128>(Q, K, V, Kc, Vc, O, o_f32, blocks, count, most, Hq, Hkv, total,
+                                    g, w, s);
+    return launch_packed_d<64>(Q, K, V, Kc, Vc, O, o_f32, blocks, count, most, Hq, Hkv, total, g, w,
+                               s);
+}
 
 cudaError_t launch_prefill(const void *Q, const void *K, const void *V,
                            const void *Kc, const void *Vc, void *O, bool o_f32,

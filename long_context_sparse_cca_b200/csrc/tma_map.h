@@ -26,15 +26,17 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tma_encode_fn()
     return fn;
 }
 
+// row_stride, plane_stride: in elements, multiples of 8; 0: contiguous.
 inline bool make_map(CUtensorMap *m, const void *ptr, int d, int64_t rows, int64_t planes,
-                     bool f16 = false)
+                     bool f16 = false, int64_t row_stride = 0, int64_t plane_stride = 0)
 {
     auto fn = tma_encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
                           static_cast<cuuint64_t>(planes)};
-    cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2,
-                             static_cast<cuuint64_t>(rows) * d * 2};
+    cuuint64_t strides[2] = {
+        static_cast<cuuint64_t>(row_stride ? row_stride : d) * 2,
+        static_cast<cuuint64_t>(plane_stride ? plane_stride : static_cast<int64_t>(rows) * d) * 2};
     cuuint32_t box[3] = {64, 128, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
