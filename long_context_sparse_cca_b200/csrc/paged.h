@@ -10,13 +10,14 @@ namespace cca {
 
 // Workspace of a paged cache (byte offsets, 256-byte aligned).
 struct PagedWorkspace {
-    size_t part_o, part_ml, tickets;               // decode: partial results
+    size_t tickets, part;                          // decode: arrivals, partial results
     size_t lens, flags, core_tmp, raw_tmp;         // fork: old lengths, new tables
     size_t lists, counts;                          // fork, compact: page moves
     size_t total;
 };
 PagedWorkspace paged_workspace(const cca_paged_cache &c);
 
+size_t paged_decode_part_bytes(const cca_paged_cache &c);
 cudaError_t launch_paged_decode(const cca_paged_cache &c, int layer, const void *q_t,
                                 const void *k_t, const void *v_t, void *o_t, bool o_f32,
                                 void *workspace, cudaStream_t s);

@@ -570,7 +570,7 @@ PagedWorkspace paged_workspace(const cca_paged_cache &c)
         return here;
     };
     w.tickets = part(sizeof(unsigned int) * c.B * c.Hkv);
-    w.part_o = w.part_ml = at;
+    w.part = part(paged_decode_part_bytes(c));
     w.lens = part(sizeof(long long) * c.B);
     w.flags = part(sizeof(int) * c.B);
     w.core_tmp = part(sizeof(int) * static_cast<size_t>(c.B) * c.core_cols);

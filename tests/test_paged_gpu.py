@@ -263,6 +263,7 @@ CASES = [  # Hq, Hkv, d, g, w, page, prompts, core pages?
     (32, 2, 128, 256, 300, 64, [2500, 255, 256, 511], True),
     (4, 1, 64, 16, ALL, 16, [300, 16, 1, 700], False),
     (4, 4, 128, 16, ALL, 32, [33, 32, 31, 2000], True),
+    (32, 2, 64, 256, 300, 16, [2500, 255, 256, 511], True),
 ]
 
 
