@@ -43,30 +43,46 @@ __device__ unsigned int g_paged_decode_status;  // kStatusCapacity, kStatusPage,
 
 namespace {
 
-constexpr int kTile = 16;
+constexpr int kPart = 16;  // rows of a part of a tile, which lie in one page
 constexpr int kCtas = 148;  // one per SM
 
-// Floats of a warp's shared memory: two partial results of r query heads
-// (m, l, O), or the scratch of a pooling.
-__host__ __device__ constexpr int warp_floats(int D, int r, int g)
+template <int D>
+struct Pd {
+    static constexpr int PARTS = 128 / D;        // of a tile: 16 or 32 rows, 8 KB
+    static constexpr int KEYS = kPart * PARTS;
+    static constexpr int ROWS = kPart * D * 2;   // bytes of a part's keys (or values)
+    static constexpr int STAGE = 2 * PARTS * ROWS;
+};
+
+// Floats of a partial result of r query heads: O [r][D], m [r], l [r].
+__host__ __device__ constexpr int part_floats(int D, int r) { return (r * (D + 2) + 3) / 4 * 4; }
+
+// Shared memory: for every warp its ring and one partial result (the ring
+// holds the other one at the end, and both together are a pooling's
+// scratch), then the list of tiles, [B + 1].
+__host__ __device__ constexpr int warp_bytes(int D, int r, int stages)
 {
-    const int part = 2 * r * (D + 2), pool = (r + 1) * g;
-    return part > pool ? part : pool;
+    return stages * 8192 + 4 * part_floats(D, r);
+}
+size_t decode_smem(int D, int r, int warps, int stages, int B)
+{
+    return static_cast<size_t>(warps) * warp_bytes(D, r, stages) + sizeof(int64_t) * (B + 1);
 }
 
+template <bool F16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1, bool f16)
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    if (f16)
+    if constexpr (F16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
-                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
-                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // (x0, x1) as a pair of the tile's type and the pair of what that leaves.
@@ -82,69 +98,109 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_
     }
 }
 
-// Tiles of a row: core tiles, then raw ones (aligned to 16 tokens).
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
+// Tiles of a row: core tiles, then raw ones (aligned to whole tiles of
+// tokens).
 struct RowTiles {
     int64_t len, ws, n_core;
     int core, all;
 };
 
+template <int KEYS>
 __device__ __forceinline__ RowTiles row_tiles(const PagedView &c, int b, bool &over)
 {
     RowTiles r;
-    const int64_t len = c.lens[b];
+    const int64_t len = __ldg(c.lens + b);
     over = len > c.longest;  // a row longer than its table is taken as free
     r.len = over || len < 0 ? 0 : len;
     const PagedRow p = paged_row(r.len, c.g, c.w);
     r.ws = p.ws;
     r.n_core = p.n_core;
-    r.core = static_cast<int>((p.n_core + kTile - 1) / kTile);
-    r.all = r.len == 0 ? 0 : r.core + static_cast<int>(((r.len + kTile - 1) / kTile) - p.ws / kTile);
+    r.core = static_cast<int>((p.n_core + KEYS - 1) / KEYS);
+    r.all = r.len == 0 ? 0 : r.core + static_cast<int>(((r.len + KEYS - 1) / KEYS) - p.ws / KEYS);
     return r;
 }
 
-// Where a warp stands in the list of tiles.
-struct Place {
-    int b, h, i;    // row, head, tile within the pair
-    RowTiles row;
-};
+__device__ __forceinline__ void put4(void *o_t, int o_f32, int64_t at, float4 y)
+{
+    if (o_f32)
+        *reinterpret_cast<float4 *>(static_cast<float *>(o_t) + at) = y;
+    else
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(o_t) + at) =
+            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+}
 
-// One tile: rows [lo, hi) of it count; their page (or none).
-struct Tile {
-    bool core;
-    int lo, hi;       // of 16
-    int page, slot;   // slot of the tile's first row
-    bool newest;      // row hi - 1 is the token that this launch appends
-};
+__device__ __forceinline__ void put8(void *o_t, int o_f32, int64_t at, const float (&y)[8])
+{
+    if (o_f32) {
+        float4 *to = reinterpret_cast<float4 *>(static_cast<float *>(o_t) + at);
+        to[0] = make_float4(y[0], y[1], y[2], y[3]);
+        to[1] = make_float4(y[4], y[5], y[6], y[7]);
+    } else {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(o_t) + at) =
+            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                       pack_bf16x2(y[6], y[7]));
+    }
+}
 
-template <int D, int WARPS, bool WIDE, bool STEP>
+// A tile in its stage: bits 0-5: first row that counts, 6-11: one behind the
+// last, kPage << i: part i has a page.
+constexpr int kCore = 1 << 12, kNewest = 1 << 13, kFirst = 1 << 14, kEnds = 1 << 15,
+              kPage = 1 << 16;
+
+// What a pair costs a warp beside its tiles, and what a pooling does, in
+// tiles.
+constexpr int kPairTiles = 3, kPoolTiles = 4;
+
+template <int D, int WARPS, int STAGES, bool WIDE, bool STEP>
 __global__ void __launch_bounds__(WARPS * 32, 1)
     paged_decode_kernel(PagedView c, const uint16_t *__restrict__ q_t,
                         const uint16_t *__restrict__ k_t, const uint16_t *__restrict__ v_t,
                         void *__restrict__ o_t, int o_f32, float scale_log2,
                         float *__restrict__ part, unsigned int *__restrict__ tickets)
 {
-    constexpr int THREADS = WARPS * 32;
-    constexpr int KC = D / 32, VH = D / 64;
+    using P = Pd<D>;
+    constexpr int kWarps = WARPS, kThreads = WARPS * 32;
+    constexpr int CH = D / 8;        // 16-byte chunks of a row
+    constexpr int VH = D / 64;       // 128-byte pieces of a row
+    constexpr int QR = WIDE ? 2 : 1; // query rows of a thread
     const int r = c.Hq / c.Hkv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, qi = lane >> 2, qj = lane & 3;
-    const int PS = r * (D + 2);             // floats of a partial result
-    const int WF = warp_floats(D, r, c.g);  // of a warp's shared memory
-    extern __shared__ float smem[];
-    float *mine = smem + warp * WF;
-    // tiles of the rows before b, [B + 1]
-    int64_t *before = reinterpret_cast<int64_t *>(smem + (WARPS * WF + 1) / 2 * 2);
-    __shared__ int64_t sums[WARPS];
-    __shared__ int ids[2 * WARPS];          // pairs of the warps' partial results, -1: none
-    __shared__ int last_s[2];
+    const int PS = part_floats(D, r);
+    extern __shared__ __align__(16) char smem[];
+    const int WB = warp_bytes(D, r, STAGES);
+    char *ring = smem + warp * WB;
+    // a warp's two partial results: one begun before its stretch, and the last one
+    auto entry_at = [&](int e) {
+        return reinterpret_cast<float *>(smem + (e >> 1) * WB + (e & 1 ? 0 : STAGES * P::STAGE));
+    };
+    // of the rows before b: 2^13 times their tiles and the number of those
+    // that have any
+    int64_t *before = reinterpret_cast<int64_t *>(smem + kWarps * WB);
+    auto tiles_before = [&](int b) { return before[b] >> 13; };
+    __shared__ int64_t sums[kWarps];
+    __shared__ int4 meta[kWarps][STAGES];  // row, head and flags of the tiles in the ring
+    __shared__ int ids[2 * kWarps];        // pairs of the partial results, -1: none
+    __shared__ int pools_s[kWarps];
+    __shared__ int3 join_s[2];  // parts to join (0: not here), CTA of the first, its slot
 
-    if (tid < 2 * WARPS) ids[tid] = -1;
+    if (tid < 2 * kWarps) ids[tid] = -1;
     {  // the list: each thread sums its rows, then a scan over the block
-        const int per = (c.B + THREADS - 1) / THREADS;
+        const int per = (c.B + kThreads - 1) / kThreads;
         const int b0 = min(tid * per, c.B), b1 = min(b0 + per, c.B);
         int64_t n = 0;
         for (int b = b0; b < b1; ++b) {
             bool over;
-            n += row_tiles(c, b, over).all;
+            before[b] = n;
+            const int all = row_tiles<P::KEYS>(c, b, over).all;
+            n += (static_cast<int64_t>(all) << 13) + (all > 0);
             if (over && blockIdx.x == 0) atomicOr(&g_paged_decode_status, kStatusCapacity);
         }
         int64_t x = n;
@@ -155,86 +211,333 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         }
         if (lane == 31) sums[warp] = x;
         __syncthreads();
-        int64_t at = x - n;
-        for (int w = 0; w < warp; ++w) at += sums[w];
-        for (int b = b0; b < b1; ++b) {
-            bool over;
-            before[b] = at;
-            at += row_tiles(c, b, over).all;
-        }
-        if (b0 < c.B && b1 == c.B) before[c.B] = at;
+        int64_t add = x - n;
+        for (int w = 0; w < warp; ++w) add += sums[w];
+        for (int b = b0; b < b1; ++b) before[b] += add;
+        if (b0 < c.B && b1 == c.B) before[c.B] = add + n;
         __syncthreads();
     }
 
+    const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    const int cc = lane % CH;  // this lane's chunk of the rows it copies
+    // 16 rows of keys or values to shared memory at `to`; those outside
+    // [tlo, thi) become zeros, row `fresh` comes from `in`.  Row x's chunk y
+    // lies at chunk y ^ (x % 8) of its 128 bytes, so that the fragments'
+    // reads below, 8 lanes at a time, meet no bank twice.
+    constexpr int RPC = 32 / CH;     // rows that the warp copies at once
+    constexpr int NU = 8 / RPC;      // copies until x % 8 comes again
+    uint32_t to_off[NU];
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        const int x = u * RPC + lane / CH;
+        to_off[u] = (cc >> 3) * (kPart * 128) + x * 128 + (((cc & 7) ^ x) << 4);
+    }
+    const int from_off = lane / CH * D + cc * 8;
+    auto copy_rows = [&](uint32_t to, const uint16_t *from, const uint16_t *in, int tlo, int thi,
+                         int fresh) {
+        const uint16_t *src = from + from_off;
+#pragma unroll
+        for (int u = 0; u < kPart / RPC; ++u) {
+            const int x = u * RPC + lane / CH;
+            const bool is_new = STEP && x == fresh;
+            copy16(to + to_off[u % NU] + u / NU * 1024, is_new ? in + cc * 8 : src + u * RPC * D,
+                   is_new || (x >= tlo && x < thi));
+        }
+    };
+    auto commit = [&]() { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    auto chunk = [&](const char *tile, int x, int y) {
+        return *reinterpret_cast<const uint4 *>(tile + (y >> 3) * (kPart * 128) + x * 128 +
+                                                (((y & 7) ^ (x & 7)) << 4));
+    };
+    // Queries of the pair as fragments: rows qi and (WIDE) qi + 8, the
+    // dims 64 h + 16 qj .. + 15.
+    uint4 qf[QR][2 * VH];
+    float q_scale[QR];
+    auto load_q = [&](int b, int h, bool core) {
+#pragma unroll
+        for (int x = 0; x < QR; ++x) {
+            const int qrow = x * 8 + qi;
+            q_scale[x] = scale_log2;
+#pragma unroll
+            for (int e = 0; e < 2 * VH; ++e)
+                qf[x][e] = qrow < r
+                               ? __ldg(reinterpret_cast<const uint4 *>(
+                                     q_t +
+                                     (static_cast<int64_t>(b) * c.Hq + h * r + qrow) * D +
+                                     (e >> 1) * 64 + qj * 16 + (e & 1) * 8))
+                               : make_uint4(0u, 0u, 0u, 0u);
+            if (!core) continue;
+            uint32_t top = 0;  // the row's largest magnitude, as bf16 bits
+#pragma unroll
+            for (int e = 0; e < 2 * VH; ++e)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t v = (&qf[x][e].x)[u] & 0x7fff7fffu;
+                    top = max(top, max(v & 0xffffu, v >> 16));
+                }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // entries times 2^(13 - e), e: exponent of the largest one
+            // (zero rows and exponents that leave the range: the nearest)
+            const int e2 = top == 0 ? 13 : static_cast<int>(top >> 7) - 127;
+            const int up = max(-100, min(100, 13 - e2));
+            const float f = __int_as_float((127 + up) << 23);
+            q_scale[x] = scale_log2 * __int_as_float((127 - up) << 23);
+#pragma unroll
+            for (int e = 0; e < 2 * VH; ++e)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t &v = (&qf[x][e].x)[u];
+                    v = pack_f16x2(bf16_lo(v) * f, bf16_hi(v) * f);
+                }
+        }
+    };
+
+    // S of a tile: rows qi and qi + 8, keys 8 n + 2 qj + e.
+    auto scores = [&](const char *tile, float (&s)[2][4], auto f16_c) {
+        constexpr bool F16 = decltype(f16_c)::value;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+#pragma unroll
+            for (int x = 0; x < 2 * VH; ++x) {
+                const uint4 k = chunk(tile, n * 8 + qi, (x >> 1) * 8 + qj * 2 + (x & 1));
+                const uint4 a = qf[0][x];
+                const uint4 z = WIDE ? qf[QR - 1][x] : make_uint4(0u, 0u, 0u, 0u);
+                mma16816<F16>(s[n], a.x, z.x, a.y, z.y, k.x, k.y);
+                mma16816<F16>(s[n], a.z, z.z, a.w, z.w, k.z, k.w);
+            }
+        }
+    };
+
+    // The append of token t of row b for one head: its rows to its page, and
+    // the pooling of the group it completes (section 全局感知池化): the scores
+    // of the group's keys against this token's queries, a softmax for each
+    // query head, and the sums of keys and values weighted by their mean.
+    auto append = [&](int b, int h, int64_t t) {
+        using VT = typename RowVec<D>::T;
+        const int mask = (1 << c.shift) - 1, g = c.g;
+        const uint16_t *kin = k_t + (static_cast<int64_t>(b) * c.Hkv + h) * D;
+        const uint16_t *vin = v_t + (static_cast<int64_t>(b) * c.Hkv + h) * D;
+        // the group's tiles of 16 tokens (g <= 256: at most 17), token t in
+        // the last one, and their pages; the tables are read at once, and
+        // the counts with the keys and values, whose copies need no counts
+        const bool ends = c.core_cols > 0 && (t + 1) % g == 0;
+        const int64_t first = ends ? t - g + 1 : t, j = t / g, tile0 = first / kPart;
+        const int n_tiles = static_cast<int>(t / kPart - tile0) + 1;
+        const int skip = static_cast<int>(first - tile0 * kPart);
+        const VT kx = reinterpret_cast<const VT *>(kin)[lane];
+        const VT vx = reinterpret_cast<const VT *>(vin)[lane];
+        const int id = lane < n_tiles ? page_at(c.raw_table, b, c.raw_cols,
+                                                ((tile0 + lane) * kPart) >> c.shift, c.raw_pages)
+                                      : 0;
+        const int out = ends ? page_at(c.core_table, b, c.core_cols, j >> c.shift, c.core_pages) : 0;
+        const int page = __shfl_sync(0xffffffffu, id, n_tiles - 1);
+        // (count 1: the page is the row's own)
+        const bool mine = page >= 0 && __ldg(c.raw_ref + page) == 1;
+        const bool out_mine = !ends || (out >= 0 && __ldg(c.core_ref + out) == 1);
+        auto put_row = [&]() {
+            const int64_t at = page_row<D>(page, h, c.Hkv, c.shift, static_cast<int>(t) & mask);
+            reinterpret_cast<VT *>(c.k_raw + at)[lane] = kx;
+            reinterpret_cast<VT *>(c.v_raw + at)[lane] = vx;
+        };
+        if (!ends || __any_sync(0xffffffffu, id < 0 || out < 0)) {
+            if (mine) put_row();
+            if (lane == 0 && (ends || !mine)) atomicOr(&g_paged_decode_status, kStatusPage);
+            return;
+        }
+        // scratch: scores [r][g], weights [g], a factor for each head, and
+        // before them room for tiles of keys or values (one at least)
+        const int n_scratch = (r + 1) * g + r;
+        float *logit = reinterpret_cast<float *>(ring + WB) - n_scratch;
+        float *weight = logit + r * g, *factor = weight + g;
+        const int slots = (WB - 4 * n_scratch) / P::ROWS;
+        const bool at_once = 2 * n_tiles <= slots;  // keys and values fit
+        auto load = [&](int i0, int n, bool v, int slot) {
+            for (int i = 0; i < n; ++i) {
+                const int64_t p = (tile0 + i0 + i) * kPart;
+                const int pg = __shfl_sync(0xffffffffu, id, i0 + i);
+                const int thi = static_cast<int>(min(static_cast<int64_t>(kPart), t + 1 - p));
+                copy_rows(ring_s + (slot + i) * P::ROWS,
+                          (v ? c.v_raw : c.k_raw) +
+                              page_row<D>(pg, h, c.Hkv, c.shift, static_cast<int>(p) & mask),
+                          v ? vin : kin, i0 + i == 0 ? skip : 0, thi, p + thi == t + 1 ? thi - 1 : -1);
+            }
+            commit();
+        };
+        auto wait = [&]() {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            __syncwarp();
+        };
+        const int step = at_once ? n_tiles : slots;
+        for (int i0 = 0; i0 < n_tiles; i0 += step) {
+            load(i0, min(step, n_tiles - i0), false, 0);
+            if (at_once) load(0, n_tiles, true, n_tiles);
+            if (i0 == 0) load_q(b, h, false);
+            wait();
+            for (int i = 0; i < min(step, n_tiles - i0); ++i) {
+                float s[2][4];
+                scores(ring + i * P::ROWS, s, std::false_type{});
+#pragma unroll
+                for (int x = 0; x < QR; ++x)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int pos = (i0 + i) * kPart + n * 8 + qj * 2 + e - skip;
+                            if (pos >= 0 && pos < g && x * 8 + qi < r)
+                                logit[(x * 8 + qi) * g + pos] = s[n][2 * x + e] * scale_log2;
+                        }
+            }
+            __syncwarp();
+        }
+        // softmax over the scores of each head: four heads at once, 8 lanes each
+        for (int k0 = 0; k0 < r; k0 += 4) {
+            const int k = k0 + (lane >> 3);
+            float *y = logit + k * g;
+            float mx = -INFINITY, sum = 0.f;
+            if (k < r)
+                for (int i = lane & 7; i < g; i += 8) mx = fmaxf(mx, y[i]);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (k < r)
+                for (int i = lane & 7; i < g; i += 8) sum += y[i] = fast_exp2(y[i] - mx);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (k < r && (lane & 7) == 0) factor[k] = 1.0f / (sum * static_cast<float>(r));
+        }
+        __syncwarp();
+        for (int i = lane; i < g; i += 32) {
+            float a = 0.f;
+            for (int k = 0; k < r; ++k) a = fmaf(logit[k * g + i], factor[k], a);
+            weight[i] = a;
+        }
+        __syncwarp();
+        if (mine) put_row();
+        if (!mine || !out_mine) {
+            if (lane == 0) atomicOr(&g_paged_decode_status, kStatusPage);
+            return;
+        }
+        const int64_t to = page_row<D>(out, h, c.Hkv, c.shift, static_cast<int>(j) & mask);
+        bool over = false;
+        for (int v = 0; v < 2; ++v) {
+            float acc[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+            for (int i0 = 0; i0 < n_tiles; i0 += step) {
+                const int n = min(step, n_tiles - i0);
+                if (!at_once) {
+                    load(i0, n, v, 0);
+                    wait();
+                }
+                for (int i = 0; i < n; ++i) {
+                    const char *tile = ring + ((at_once && v ? n_tiles : 0) + i) * P::ROWS;
+#pragma unroll
+                    for (int x = lane / CH; x < kPart; x += 32 / CH) {
+                        const int pos = (i0 + i) * kPart + x - skip;
+                        const float a = pos >= 0 && pos < g ? weight[pos] : 0.f;
+                        const uint4 y = chunk(tile, x, cc);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            acc[2 * e] = fmaf(a, bf16_lo((&y.x)[e]), acc[2 * e]);
+                            acc[2 * e + 1] = fmaf(a, bf16_hi((&y.x)[e]), acc[2 * e + 1]);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+#pragma unroll
+            for (int o = CH; o < 32; o <<= 1)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] += __shfl_xor_sync(0xffffffffu, acc[e], o);
+            if (lane < CH) {
+                uint4 y;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    (&y.x)[e] = pack_f16x2(clamp_f16(acc[2 * e], over), clamp_f16(acc[2 * e + 1], over));
+                *reinterpret_cast<uint4 *>((v ? c.v_core : c.k_core) + to + cc * 8) = y;
+            }
+        }
+        if (over) atomicOr(&g_paged_decode_status, kStatusRange);
+    };
+
+    auto pooled = [&](int b) {
+        return before[b + 1] > before[b] && c.core_cols > 0 && __ldg(c.lens + b) % c.g == 0;
+    };
     // Rows without tokens have a zero output; the newest token of the others
     // is appended.  No tile reads what is written here: its key and value
     // come from the inputs, and the core row of the group it completes is not
-    // yet among those that it sees.  The last warps begin, which have no
-    // tiles when there are few.
-    for (int64_t pair = static_cast<int64_t>(gridDim.x) * WARPS - 1 - (blockIdx.x * WARPS + warp);
-         pair < static_cast<int64_t>(c.B) * c.Hkv;
-         pair += static_cast<int64_t>(gridDim.x) * WARPS) {
-        const int b = static_cast<int>(pair / c.Hkv), h = static_cast<int>(pair - static_cast<int64_t>(b) * c.Hkv);
-        const int64_t orow = static_cast<int64_t>(b) * c.Hq + h * r;
+    // yet among those that it sees.  The pairs go round the CTAs, the last
+    // ones first, which have no tiles when there are few.
+    const int64_t pairs = static_cast<int64_t>(c.B) * c.Hkv;
+    const int64_t pair0 = kCtas - 1 - static_cast<int>(blockIdx.x) + kCtas * static_cast<int64_t>(warp);
+    if (STEP) {  // groups that this warp is going to pool
+        int pools = 0;
+        for (int64_t pair = pair0; pair < pairs; pair += kCtas * kWarps)
+            pools += pooled(static_cast<int>(pair / c.Hkv));
+        if (lane == 0) pools_s[warp] = pools;
+        __syncthreads();
+    }
+    for (int64_t pair = pair0; pair < pairs; pair += kCtas * kWarps) {
+        const int b = static_cast<int>(pair / c.Hkv);
+        const int h = static_cast<int>(pair - static_cast<int64_t>(b) * c.Hkv);
         if (before[b + 1] == before[b]) {
-            for (int x = lane; x < r * D; x += 32) {
-                if (o_f32)
-                    static_cast<float *>(o_t)[orow * D + x] = 0.f;
-                else
-                    static_cast<uint16_t *>(o_t)[orow * D + x] = 0;
-            }
-            continue;
+            const int64_t orow = static_cast<int64_t>(b) * c.Hq + h * r;
+            for (int x = lane * 4; x < r * D; x += 128)
+                put4(o_t, o_f32, orow * D + x, make_float4(0.f, 0.f, 0.f, 0.f));
+        } else if (STEP) {
+            append(b, h, __ldg(c.lens + b) - 1);
         }
-        if (!STEP) continue;
-        using VT = typename RowVec<D>::T;
-        const int64_t t = c.lens[b] - 1;
-        const int mask = (1 << c.shift) - 1;
-        const int page =
-            own_page_at(c.raw_table, c.raw_ref, b, c.raw_cols, t >> c.shift, c.raw_pages);
-        if (page < 0) {
-            if (lane == 0) atomicOr(&g_paged_decode_status, kStatusPage);
-            continue;
-        }
-        const int64_t at = page_row<D>(page, h, c.Hkv, c.shift, static_cast<int>(t) & mask);
-        reinterpret_cast<VT *>(c.k_raw + at)[lane] =
-            reinterpret_cast<const VT *>(k_t + pair * D)[lane];
-        reinterpret_cast<VT *>(c.v_raw + at)[lane] =
-            reinterpret_cast<const VT *>(v_t + pair * D)[lane];
-        if (c.core_cols == 0 || (t + 1) % c.g != 0) continue;
-        const int64_t first = t - c.g + 1, j = t / c.g;
-        int out = own_page_at(c.core_table, c.core_ref, b, c.core_cols, j >> c.shift, c.core_pages);
-        for (int i = lane; i < c.g; i += 32)
-            if (page_at(c.raw_table, b, c.raw_cols, (first + i) >> c.shift, c.raw_pages) < 0)
-                out = -1;
-        if (__any_sync(0xffffffffu, out < 0)) {
-            if (lane == 0) atomicOr(&g_paged_decode_status, kStatusPage);
-            continue;
-        }
-        auto old = [&](const uint16_t *pool, const uint16_t *in, int i) {
-            if (i == c.g - 1) return in + pair * D;
-            const int64_t pos = first + i;
-            const int pg = page_at(c.raw_table, b, c.raw_cols, pos >> c.shift, c.raw_pages);
-            return pool + page_row<D>(pg, h, c.Hkv, c.shift, static_cast<int>(pos) & mask);
-        };
-        const int64_t to = page_row<D>(out, h, c.Hkv, c.shift, static_cast<int>(j) & mask);
-        const bool over = pool_group_warp<D>(
-            [&](int i) { return old(c.k_raw, k_t, i); }, [&](int i) { return old(c.v_raw, v_t, i); },
-            [&](int k) { return q_t + (orow + k) * D; }, r, c.g, scale_log2, mine, c.k_core + to,
-            c.v_core + to);
-        if (over && lane == 0) atomicOr(&g_paged_decode_status, kStatusRange);
-        __syncwarp();
     }
 
-    // This CTA's stretch of the list (at least a tile for each warp, as long
-    // as there are enough), and this warp's part of it.
-    auto first_of = [&](int b) { return before[b] * c.Hkv; };
-    const int64_t total = first_of(c.B);
-    if (total == 0) return;
-    const int64_t n_ctas = min(static_cast<int64_t>(gridDim.x), (total + WARPS - 1) / WARPS);
+    // The list of the tiles, row by row and head by head, each pair preceded
+    // by what it costs beside them, is cut into equal stretches: one for each
+    // CTA (enough for each warp, as long as there is), and in it for each warp.
+    auto first_of = [&](int b) { return tiles_before(b) * c.Hkv; };
+    auto cost_of = [&](int b) {
+        return (tiles_before(b) + kPairTiles * (before[b] & 8191)) * c.Hkv;
+    };
+    const int64_t total = cost_of(c.B);
+    const int n_ctas =
+        static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + kWarps - 1) / kWarps));
     if (blockIdx.x >= n_ctas) return;
-    const int64_t cta_lo = total * blockIdx.x / n_ctas, cta_hi = total * (blockIdx.x + 1) / n_ctas;
-    const int64_t lo = cta_lo + (cta_hi - cta_lo) * warp / WARPS;
-    const int64_t hi = cta_lo + (cta_hi - cta_lo) * (warp + 1) / WARPS;
+    // the first tile at or behind place x of the list
+    auto tile_from = [&](int64_t x) {
+        if (x >= total) return first_of(c.B);
+        int a = 0, z = c.B - 1;
+        while (a < z) {
+            const int mid = (a + z + 1) >> 1;
+            if (cost_of(mid) <= x)
+                a = mid;
+            else
+                z = mid - 1;
+        }
+        const int64_t n = tiles_before(a + 1) - tiles_before(a);
+        const int64_t in_row = x - cost_of(a), h = in_row / (n + kPairTiles);
+        return first_of(a) + h * n + max(static_cast<int64_t>(0), in_row - h * (n + kPairTiles) - kPairTiles);
+    };
+    // the CTA that has tile i of a head's n in row b
+    auto cta_of = [&](int b, int h, int64_t n, int64_t i) {
+        const int64_t x = cost_of(b) + h * (n + kPairTiles) + kPairTiles + i;
+        return static_cast<int>(((x + 1) * n_ctas - 1) / total);
+    };
+    const int64_t my_lo = total * blockIdx.x / n_ctas, my_hi = total * (blockIdx.x + 1) / n_ctas;
+    const int64_t cta_lo = tile_from(my_lo), cta_hi = tile_from(my_hi);
+    int64_t lo = my_lo, hi = my_lo;
+    {
+        int all = 0, upto = 0;
+        for (int w = 0; STEP && w < kWarps; ++w) all += pools_s[w];
+        for (int w = 0; w <= warp; ++w) {
+            if (STEP) upto += pools_s[w];
+            lo = hi;
+            hi = my_lo + (my_hi - my_lo + kPoolTiles * all) * (w + 1) / kWarps - kPoolTiles * upto;
+            hi = w + 1 == kWarps ? my_hi : max(lo, min(my_hi, hi));
+        }
+        lo = tile_from(lo);
+        hi = tile_from(hi);
+    }
+    const int n_tiles = static_cast<int>(hi - lo);
 
     // The last row whose tiles begin at or before x.
     auto row_at = [&](int64_t x) {
@@ -248,409 +551,397 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         }
         return a;
     };
-    Place at = {};
-    int ids_from = 0, ids_mine = 0;  // pages of tiles ids_from + lane of the pair
-    auto load_ids = [&]() {
-        ids_from = at.i;
-        const int i = at.i + lane;
-        ids_mine = -1;
-        if (i < at.row.core)
-            ids_mine = page_at(c.core_table, at.b, c.core_cols,
-                               (static_cast<int64_t>(i) * kTile) >> c.shift, c.core_pages);
-        else if (i < at.row.all)
-            ids_mine = page_at(c.raw_table, at.b, c.raw_cols,
-                               ((at.row.ws / kTile + (i - at.row.core)) * kTile) >> c.shift,
-                               c.raw_pages);
-    };
-    auto tile_at = [&]() {
-        Tile t;
-        t.core = at.i < at.row.core;
-        if (at.i - ids_from >= 32) load_ids();
-        t.page = __shfl_sync(0xffffffffu, ids_mine, at.i - ids_from);
-        if (t.core) {
-            const int64_t p = static_cast<int64_t>(at.i) * kTile;
-            t.slot = static_cast<int>(p) & ((1 << c.shift) - 1);
-            t.lo = 0;
-            t.hi = static_cast<int>(min(static_cast<int64_t>(kTile), at.row.n_core - p));
-            t.newest = false;
-        } else {
-            const int64_t p = (at.row.ws / kTile + (at.i - at.row.core)) * kTile;
-            t.slot = static_cast<int>(p) & ((1 << c.shift) - 1);
-            t.lo = static_cast<int>(max(static_cast<int64_t>(0), at.row.ws - p));
-            t.hi = static_cast<int>(min(static_cast<int64_t>(kTile), at.row.len - p));
-            t.newest = STEP && p + t.hi == at.row.len;
-        }
-        return t;
-    };
-    auto next_place = [&]() {
-        if (++at.i < at.row.all) return;
-        at.i = 0;
-        if (++at.h == c.Hkv) {
-            at.h = 0;
-            bool over;
-            do {
-                ++at.b;
-                at.row = row_tiles(c, at.b, over);
-            } while (at.row.all == 0);
-        }
-        load_ids();
-    };
 
-    uint4 kf[2][KC], vf[4][VH];
-    auto load_k = [&](const Tile &t) {
-        const uint16_t *base = (t.core ? c.k_core : c.k_raw) +
-                               page_row<D>(max(t.page, 0), at.h, c.Hkv, c.shift, t.slot) + qj * 8;
-        const uint16_t *in = k_t + (static_cast<int64_t>(at.b) * c.Hkv + at.h) * D + qj * 8;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int row = n * 8 + qi;
-            const uint16_t *src = base + row * D;
-            bool ok = row >= t.lo && row < t.hi && t.page >= 0;
-            if (STEP && t.newest && row == t.hi - 1) {
-                src = in;
-                ok = true;
-            }
-#pragma unroll
-            for (int x = 0; x < KC; ++x)
-                kf[n][x] = ok ? ldg_stream(src + x * 32) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-    auto load_v = [&](const Tile &t, int b, int h) {
-        const uint16_t *base = (t.core ? c.v_core : c.v_raw) +
-                               page_row<D>(max(t.page, 0), h, c.Hkv, c.shift, t.slot) + qi * 8;
-        const uint16_t *in = v_t + (static_cast<int64_t>(b) * c.Hkv + h) * D + qi * 8;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int row = (n >> 1) * 8 + qj * 2 + (n & 1);
-            const uint16_t *src = base + row * D;
-            bool ok = row >= t.lo && row < t.hi && t.page >= 0;
-            if (STEP && t.newest && row == t.hi - 1) {
-                src = in;
-                ok = true;
-            }
-#pragma unroll
-            for (int x = 0; x < VH; ++x)
-                vf[n][x] = ok ? ldg_stream(src + x * 64) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-
-    // Queries of the pair as fragments: rows qi and (WIDE) qi + 8.
-    constexpr int QR = WIDE ? 2 : 1;
-    uint4 qf[QR][KC];
-    float q_scale[QR];
-    auto load_q = [&](int b, int h, bool core) {
-#pragma unroll
-        for (int x = 0; x < QR; ++x) {
-            const int row = x * 8 + qi;
-            q_scale[x] = scale_log2;
-#pragma unroll
-            for (int e = 0; e < KC; ++e)
-                qf[x][e] = row < r ? __ldg(reinterpret_cast<const uint4 *>(
-                                         q_t + (static_cast<int64_t>(b) * c.Hq + h * r + row) * D +
-                                         e * 32 + qj * 8))
-                                   : make_uint4(0u, 0u, 0u, 0u);
-            if (!core) continue;
-            uint32_t top = 0;  // the row's largest magnitude, as bf16 bits
-#pragma unroll
-            for (int e = 0; e < KC; ++e)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t v = (&qf[x][e].x)[u] & 0x7fff7fffu;
-                    top = max(top, max(v & 0xffffu, v >> 16));
-                }
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // entries times 2^(13 - e), e: exponent of the largest one (zero
-            // rows and exponents that leave the type's range: the nearest)
-            const int e2 = top == 0 ? 13 : static_cast<int>(top >> 7) - 127;
-            const int up = max(-100, min(100, 13 - e2));
-            const float f = __int_as_float((127 + up) << 23);
-            q_scale[x] = scale_log2 * __int_as_float((127 - up) << 23);
-#pragma unroll
-            for (int e = 0; e < KC; ++e)
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    uint32_t &v = (&qf[x][e].x)[u];
-                    v = pack_f16x2(bf16_lo(v) * f, bf16_hi(v) * f);
-                }
-        }
-    };
-
-    float o[D / 8][4], m[QR], l[QR];
-    auto reset = [&]() {
-#pragma unroll
-        for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-#pragma unroll
-        for (int x = 0; x < QR; ++x) {
-            m[x] = -INFINITY;
-            l[x] = 0.f;
-        }
-    };
-    // S, softmax and P V of the tile in registers.
-    auto scores = [&](bool f16, float (&s)[2][4]) {
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
-#pragma unroll
-            for (int x = 0; x < KC; ++x) {
-                const uint4 k = kf[n][x], a = qf[0][x];
-                const uint4 z = WIDE ? qf[QR - 1][x] : make_uint4(0u, 0u, 0u, 0u);
-                mma16816(s[n], a.x, z.x, a.y, z.y, k.x, k.y, f16);
-                mma16816(s[n], a.z, z.z, a.w, z.w, k.z, k.w, f16);
-            }
-        }
-    };
-    auto add_tile = [&](const Tile &t, float (&s)[2][4], auto f16_c) {
-        constexpr bool F16 = decltype(f16_c)::value;
-        uint32_t ph[QR][2], pl[QR][2];
-#pragma unroll
-        for (int x = 0; x < QR; ++x) {
-            float top = -INFINITY;
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = n * 8 + qj * 2 + e;
-                    float &y = s[n][2 * x + e];
-                    // a missing page leaves the newest row alone
-                    const bool ok = t.page >= 0 ? row >= t.lo && row < t.hi
-                                                : t.newest && row == t.hi - 1;
-                    y = ok ? y * q_scale[x] : -INFINITY;
-                    top = fmaxf(top, y);
-                }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float to = fmaxf(m[x], top);
-            const float use = to == -INFINITY ? 0.f : to;
-            if (__any_sync(0xffffffffu, to > m[x])) {
-                const float f = fast_exp2(m[x] - use);
-                l[x] *= f;
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    o[n][2 * x] *= f;
-                    o[n][2 * x + 1] *= f;
-                    if (!WIDE) {
-                        o[n][2] *= f;
-                        o[n][3] *= f;
-                    }
-                }
-                m[x] = to;
-            }
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float p0 = fast_exp2(s[n][2 * x] - use), p1 = fast_exp2(s[n][2 * x + 1] - use);
-                l[x] += p0 + p1;
-                split2<F16>(p0, p1, ph[x][n], pl[x][n]);
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < VH; ++h)
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const uint32_t v0 = (&vf[0][h].x)[u], v1 = (&vf[1][h].x)[u];
-                const uint32_t v2 = (&vf[2][h].x)[u], v3 = (&vf[3][h].x)[u];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t sel = e ? 0x7632 : 0x5410;
-                    const uint32_t b0 = __byte_perm(v0, v1, sel), b1 = __byte_perm(v2, v3, sel);
-                    float(&acc)[4] = o[h * 8 + u * 2 + e];
-                    if constexpr (WIDE) {
-                        mma16816(acc, ph[0][0], ph[1][0], ph[0][1], ph[1][1], b0, b1, F16);
-                        mma16816(acc, pl[0][0], pl[1][0], pl[0][1], pl[1][1], b0, b1, F16);
-                    } else {
-                        mma16816(acc, ph[0][0], pl[0][0], ph[0][1], pl[0][1], b0, b1, F16);
-                    }
-                }
-            }
-    };
-    auto put = [&](int64_t at, float y) {
-        if (o_f32)
-            static_cast<float *>(o_t)[at] = y;
-        else
-            static_cast<uint16_t *>(o_t)[at] = bf16_bits(y);
-    };
-    // The result of the tiles so far: the pair's output if they are all of
-    // it, else a partial result in shared memory.
-    auto finish = [&](int b, int h, bool whole, int entry) {
-        float *to = mine + entry * PS;
-#pragma unroll
-        for (int x = 0; x < QR; ++x) {
-            float sum = l[x];
-            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            const int row = x * 8 + qi;
-            if (row >= r) continue;
-            const float inv = whole ? (sum > 0.f ? 1.0f / sum : 0.f) : 1.f;
-            const int64_t orow = (static_cast<int64_t>(b) * c.Hq + h * r + row) * D;
-#pragma unroll
-            for (int hh = 0; hh < VH; ++hh)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int n = 0; n < 8; ++n) {
-                        const float(&a)[4] = o[hh * 8 + n];
-                        const float y = (WIDE ? a[2 * x + e] : a[e] + a[2 + e]) * inv;
-                        const int dim = hh * 64 + (2 * qj + e) * 8 + n;
-                        if (whole)
-                            put(orow + dim, y);
-                        else
-                            to[row * D + dim] = y;
-                    }
-            if (!whole && qj == 0) {
-                to[r * D + row] = m[x];
-                to[r * D + r + row] = sum;
-            }
-        }
-        if (!whole && lane == 0) ids[warp * 2 + entry] = b * c.Hkv + h;
-    };
-
-    if (lo < hi) {
+    if (n_tiles > 0) {
         bool over, bad = false;
-        at.b = row_at(lo);
-        at.row = row_tiles(c, at.b, over);
-        const int64_t in_row = lo - first_of(at.b);
-        at.h = static_cast<int>(in_row / at.row.all);
-        at.i = static_cast<int>(in_row - static_cast<int64_t>(at.h) * at.row.all);
+        int at_b = row_at(lo), at_h, at_i;  // row, head, tile of the pair: the next one to ask for
+        RowTiles row = row_tiles<P::KEYS>(c, at_b, over);
+        {
+            const int64_t in_row = lo - first_of(at_b);
+            at_h = static_cast<int>(in_row / row.all);
+            at_i = static_cast<int>(in_row - static_cast<int64_t>(at_h) * row.all);
+        }
+        int from = 0, id = 0;  // pages of the parts PARTS * from + lane of the pair
+        auto load_ids = [&]() {
+            from = at_i;
+            const int i = at_i + lane / P::PARTS, x = lane % P::PARTS * kPart;
+            id = -1;
+            if (i < row.core)
+                id = page_at(c.core_table, at_b, c.core_cols,
+                             (static_cast<int64_t>(i) * P::KEYS + x) >> c.shift, c.core_pages);
+            else if (i < row.all)
+                id = page_at(c.raw_table, at_b, c.raw_cols,
+                             ((row.ws / P::KEYS + (i - row.core)) * P::KEYS + x) >> c.shift,
+                             c.raw_pages);
+        };
         load_ids();
-        reset();
-        bool from_start = at.i == 0, loaded = false, q_core = false;
-        int entry = 0;
-        Tile t = tile_at();
-        load_k(t);
-        load_v(t, at.b, at.h);
-        for (int64_t x = lo; x < hi; ++x) {
-            const int b = at.b, h = at.h;
-            const bool ends = at.i + 1 == at.row.all;
-            const Tile cur = t;
-            bad |= cur.page < 0;
-            if (!loaded || q_core != cur.core) {
-                load_q(b, h, cur.core);
-                loaded = true;
-                q_core = cur.core;
+
+        // Ask for the next tile.
+        int asked = 0;
+        auto ask = [&](int stage) {
+            if (at_i - from >= 32 / P::PARTS) load_ids();
+            const bool core = at_i < row.core;
+            const int64_t p = (core ? at_i : row.ws / P::KEYS + (at_i - row.core)) *
+                              static_cast<int64_t>(P::KEYS);
+            const int tlo = core ? 0 : static_cast<int>(max(static_cast<int64_t>(0), row.ws - p));
+            const int thi = static_cast<int>(min(static_cast<int64_t>(P::KEYS),
+                                                 (core ? row.n_core : row.len) - p));
+            const bool newest = STEP && !core && p + thi == row.len;
+            const int64_t in = (static_cast<int64_t>(at_b) * c.Hkv + at_h) * D;
+            int flags = tlo | thi << 6 | (core ? kCore : 0) | (newest ? kNewest : 0) |
+                        (at_i == 0 ? kFirst : 0);
+#pragma unroll
+            for (int y = 0; y < P::PARTS; ++y) {
+                const int page = __shfl_sync(0xffffffffu, id, (at_i - from) * P::PARTS + y);
+                const int plo = max(0, tlo - y * kPart), phi = min(kPart, thi - y * kPart);
+                const int64_t off =
+                    page_row<D>(max(page, 0), at_h, c.Hkv, c.shift,
+                                static_cast<int>(p + y * kPart) & ((1 << c.shift) - 1));
+                const int valid = page >= 0 ? phi : 0;
+                const int fresh = newest ? thi - 1 - y * kPart : -1;
+                const uint32_t to = ring_s + stage * P::STAGE + y * P::ROWS;
+                copy_rows(to, (core ? c.k_core : c.k_raw) + off, k_t + in, plo, valid, fresh);
+                copy_rows(to + P::PARTS * P::ROWS, (core ? c.v_core : c.v_raw) + off, v_t + in, plo,
+                          valid, fresh);
+                if (page >= 0) flags |= kPage << y;
+                bad |= page < 0 && plo < phi;
             }
-            float s[2][4];
-            scores(cur.core, s);
-            const bool more = x + 1 < hi;
-            if (more) {
-                next_place();
-                t = tile_at();
-                load_k(t);
+            if (at_i == 0 || asked == 0) {  // the pair's queries, to L1
+                const char *q = reinterpret_cast<const char *>(
+                    q_t + (static_cast<int64_t>(at_b) * c.Hq + at_h * r) * D);
+                if (lane * 128 < r * D * 2)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
             }
-            if (cur.core)
-                add_tile(cur, s, std::true_type{});
-            else
-                add_tile(cur, s, std::false_type{});
-            if (more) load_v(t, at.b, at.h);
-            if (ends || !more) {
-                const bool whole = ends && from_start;
-                finish(b, h, whole, entry);
-                entry += !whole;
-                if (more) {
-                    reset();
-                    from_start = true;
-                    loaded = false;
+            const bool ends = at_i + 1 == row.all;
+            if (lane == 0)
+                meta[warp][stage] = make_int4(at_b, at_h, flags | (ends ? kEnds : 0), 0);
+            if (!ends) {
+                ++at_i;
+                return;
+            }
+            at_i = 0;
+            if (++at_h == c.Hkv) {
+                at_h = 0;
+                do {
+                    if (++at_b >= c.B) return;  // the end of the list
+                    row = row_tiles<P::KEYS>(c, at_b, over);
+                } while (row.all == 0);
+            }
+            load_ids();
+        };
+        float o[D / 8][4], m[QR], l[QR];
+        auto reset = [&]() {
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+#pragma unroll
+            for (int x = 0; x < QR; ++x) {
+                m[x] = -INFINITY;
+                l[x] = 0.f;
+            }
+        };
+        // S, softmax and P V of a tile.
+        auto add_tile = [&](const char *tile, int flags, auto f16_c) {
+            constexpr bool F16 = decltype(f16_c)::value;
+            constexpr int NK = 2 * P::PARTS;  // keys 8 n + 2 qj + e
+            float s[NK][4];
+#pragma unroll
+            for (int y = 0; y < P::PARTS; ++y)
+                scores(tile + y * P::ROWS, *reinterpret_cast<float(*)[2][4]>(s + 2 * y), f16_c);
+            const int tlo = flags & 63, thi = flags >> 6 & 63;
+            constexpr int kAll = kPage * ((1 << P::PARTS) - 1);
+            const bool all = tlo == 0 && thi == P::KEYS && (flags & kAll) == kAll;
+            uint32_t ph[QR][NK], pl[QR][NK];
+#pragma unroll
+            for (int x = 0; x < QR; ++x) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < NK; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &y = s[n][2 * x + e];
+                        y *= q_scale[x];
+                        if (!all) {  // a missing page leaves the newest row alone
+                            const int key = n * 8 + qj * 2 + e;
+                            const bool ok = flags & (kPage << (n / 2))
+                                                ? key >= tlo && key < thi
+                                                : (flags & kNewest) && key == thi - 1;
+                            if (!ok) y = -INFINITY;
+                        }
+                        top = fmaxf(top, y);
+                    }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const float to = fmaxf(m[x], top);
+                const float use = to == -INFINITY ? 0.f : to;
+                if (__any_sync(0xffffffffu, to > m[x])) {
+                    const float f = fast_exp2(m[x] - use);
+                    l[x] *= f;
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) {
+                        o[n][2 * x] *= f;
+                        o[n][2 * x + 1] *= f;
+                        if (!WIDE) {
+                            o[n][2] *= f;
+                            o[n][3] *= f;
+                        }
+                    }
+                    m[x] = to;
+                }
+#pragma unroll
+                for (int n = 0; n < NK; ++n) {
+                    const float p0 = fast_exp2(s[n][2 * x] - use);
+                    const float p1 = fast_exp2(s[n][2 * x + 1] - use);
+                    l[x] += p0 + p1;
+                    split2<F16>(p0, p1, ph[x][n], pl[x][n]);
                 }
             }
+#pragma unroll
+            for (int y = 0; y < P::PARTS; ++y)
+#pragma unroll
+                for (int h = 0; h < VH; ++h) {
+                    uint4 v[4];
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        v[n] = chunk(tile + (P::PARTS + y) * P::ROWS,
+                                     (n >> 1) * 8 + qj * 2 + (n & 1), h * 8 + qi);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t sel = e ? 0x7632 : 0x5410;
+                            const uint32_t b0 = __byte_perm((&v[0].x)[u], (&v[1].x)[u], sel);
+                            const uint32_t b1 = __byte_perm((&v[2].x)[u], (&v[3].x)[u], sel);
+                            float(&acc)[4] = o[h * 8 + u * 2 + e];
+                            const uint32_t(&h0)[NK] = ph[0], (&l0)[NK] = pl[0];
+                            if constexpr (WIDE) {
+                                const uint32_t(&h1)[NK] = ph[QR - 1], (&l1)[NK] = pl[QR - 1];
+                                mma16816<F16>(acc, h0[2 * y], h1[2 * y], h0[2 * y + 1],
+                                              h1[2 * y + 1], b0, b1);
+                                mma16816<F16>(acc, l0[2 * y], l1[2 * y], l0[2 * y + 1],
+                                              l1[2 * y + 1], b0, b1);
+                            } else {
+                                mma16816<F16>(acc, h0[2 * y], l0[2 * y], h0[2 * y + 1],
+                                              l0[2 * y + 1], b0, b1);
+                            }
+                        }
+                }
+        };
+
+#pragma unroll 1
+        for (; asked < STAGES - 1; ++asked) {
+            if (asked < n_tiles) ask(asked);
+            commit();
+        }
+        reset();
+        bool from_start = false, q_core = false, loaded = false;
+        int stage = 0, next = STAGES - 1;
+#pragma unroll 1
+        for (int x = 0; x < n_tiles; ++x) {
+            // tile x has arrived for every lane, and every lane is done with
+            // tile x - 1, whose stage the next copies take
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+            __syncwarp();
+            if (asked < n_tiles) {
+                ask(next);
+                ++asked;
+            }
+            commit();
+            const int4 mt = meta[warp][stage];
+            const int flags = mt.z;
+            const bool core = flags & kCore;
+            if (flags & kFirst) from_start = true;
+            if (!loaded || q_core != core) {
+                load_q(mt.x, mt.y, core);
+                loaded = true;
+                q_core = core;
+            }
+            char *tile = ring + stage * P::STAGE;
+            if (core)
+                add_tile(tile, flags, std::true_type{});
+            else
+                add_tile(tile, flags, std::false_type{});
+            const bool done = x + 1 == n_tiles;
+            if ((flags & kEnds) || done) {
+                // the pair's output if this warp has seen all of it, else a
+                // partial result
+                const bool whole = from_start && (flags & kEnds);
+                if (done) __syncwarp();  // (its place is the ring, which all have read)
+                float *to = entry_at(warp * 2 + done);
+#pragma unroll
+                for (int y = 0; y < QR; ++y) {
+                    float sum = l[y];
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                    const int qrow = y * 8 + qi;
+                    if (qrow >= r) continue;
+                    const float inv = whole ? (sum > 0.f ? 1.0f / sum : 0.f) : 1.f;
+                    const int64_t orow = (static_cast<int64_t>(mt.x) * c.Hq + mt.y * r + qrow) * D;
+#pragma unroll
+                    for (int h = 0; h < VH; ++h)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float y8[8];
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) {
+                                const float(&a)[4] = o[h * 8 + n];
+                                y8[n] = (WIDE ? a[2 * y + e] : a[e] + a[2 + e]) * inv;
+                            }
+                            const int dim = h * 64 + (2 * qj + e) * 8;
+                            if (whole)
+                                put8(o_t, o_f32, orow + dim, y8);
+                            else
+                                put8(to, 1, qrow * D + dim, y8);
+                        }
+                    if (!whole && qj == 0) {
+                        to[r * D + qrow] = m[y];
+                        to[r * D + r + qrow] = sum;
+                    }
+                }
+                if (!whole && lane == 0) ids[warp * 2 + done] = mt.x * c.Hkv + mt.y;
+                reset();
+                loaded = false;
+            }
+            stage = stage + 1 == STAGES ? 0 : stage + 1;
+            next = next + 1 == STAGES ? 0 : next + 1;
         }
         if (bad && lane == 0) atomicOr(&g_paged_decode_status, kStatusPage);
     }
     __syncthreads();
 
-    // Join the warps' partial results, pair by pair.
-    int n_slots = 0;
-    int slot_pair[2];
-    for (int e = 0; e < 2 * WARPS;) {
-        const int pair = ids[e];
-        if (pair < 0) {
-            ++e;
-            continue;
-        }
-        int z = e + 1;  // entries e .. z - 1 belong to it (those without a pair aside)
-        while (z < 2 * WARPS && (ids[z] < 0 || ids[z] == pair)) ++z;
+    // Join the warps' partial results, pair by pair: an output if this CTA
+    // has all of the pair, else its partial result for the other CTAs.
+    const int my_id = lane < 2 * kWarps ? ids[lane] : -1;
+    unsigned int left = __ballot_sync(0xffffffffu, my_id >= 0);
+    int n_slots = 0, slot0_pair = -1, slot1_pair = -1;
+    while (left) {
+        const int pair = ids[__ffs(left) - 1];
+        const unsigned int group = __ballot_sync(0xffffffffu, my_id == pair);
+        left &= ~group;
         const int b = pair / c.Hkv, h = pair - b * c.Hkv;
-        const int64_t n = before[b + 1] - before[b], begin = first_of(b) + h * n;
+        const int64_t n = tiles_before(b + 1) - tiles_before(b), begin = first_of(b) + h * n;
         const bool whole = begin >= cta_lo && begin + n <= cta_hi;
-        float *to = whole ? nullptr : part + (static_cast<int64_t>(blockIdx.x) * 2 + n_slots) * PS;
-        for (int i = tid; i < r * D; i += THREADS) {
-            const int row = i / D;
-            float mx = -INFINITY, sum = 0.f, acc = 0.f;
-            for (int y = e; y < z; ++y)
-                if (ids[y] >= 0) mx = fmaxf(mx, smem[(y >> 1) * WF + (y & 1) * PS + r * D + row]);
-            const float use = mx == -INFINITY ? 0.f : mx;
-            for (int y = e; y < z; ++y) {
-                if (ids[y] < 0) continue;
-                const float *p = smem + (y >> 1) * WF + (y & 1) * PS;
-                const float f = fast_exp2(p[r * D + row] - use);
-                sum = fmaf(f, p[r * D + r + row], sum);
-                acc = fmaf(f, p[i], acc);
+        float *to = part + (static_cast<int64_t>(blockIdx.x) * 2 + n_slots) * PS;
+        // a warp for a query head: the entries' weights lane by lane, then the
+        // head's dims over the lanes
+        for (int q = warp; q < r; q += kWarps) {
+            const bool in = group >> lane & 1;
+            const float m_e = in ? entry_at(lane)[r * D + q] : -INFINITY;
+            const float l_e = in ? entry_at(lane)[r * D + r + q] : 0.f;
+            const float mx = warp_max(m_e), use = mx == -INFINITY ? 0.f : mx;
+            float f = fast_exp2(m_e - use);
+            const float sum = warp_sum(f * l_e);
+            if (whole) f *= sum > 0.f ? 1.0f / sum : 0.f;
+            const int dim = lane * 4 % D;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+            for (unsigned int x = group; x; x &= x - 1) {
+                const int e = __ffs(x) - 1;
+                const float f_e = __shfl_sync(0xffffffffu, f, e);
+                const float4 y = *reinterpret_cast<const float4 *>(entry_at(e) + q * D + dim);
+                acc.x = fmaf(f_e, y.x, acc.x);
+                acc.y = fmaf(f_e, y.y, acc.y);
+                acc.z = fmaf(f_e, y.z, acc.z);
+                acc.w = fmaf(f_e, y.w, acc.w);
             }
-            if (whole) {
-                put((static_cast<int64_t>(b) * c.Hq + h * r) * D + i, sum > 0.f ? acc / sum : 0.f);
-            } else {
-                to[i] = acc;
-                if (i - row * D == 0) {
-                    to[r * D + row] = mx;
-                    to[r * D + r + row] = sum;
-                }
+            if (lane * 4 < D) {
+                if (whole)
+                    put4(o_t, o_f32, (static_cast<int64_t>(b) * c.Hq + h * r + q) * D + dim, acc);
+                else
+                    *reinterpret_cast<float4 *>(to + q * D + dim) = acc;
+            }
+            if (!whole && lane == 0) {
+                to[r * D + q] = mx;
+                to[r * D + r + q] = sum;
             }
         }
-        if (!whole) slot_pair[n_slots++] = pair;
-        e = z;
+        if (!whole) (n_slots++ == 0 ? slot0_pair : slot1_pair) = pair;
     }
     if (n_slots == 0) return;
 
     // Pairs shared with other CTAs: the last one to arrive joins them.
-    auto cta_of = [&](int64_t x) { return ((x + 1) * n_ctas - 1) / total; };
-    __threadfence();
     __syncthreads();
     if (tid < n_slots) {
-        const int pair = slot_pair[tid == 0 ? 0 : 1], b = pair / c.Hkv, h = pair - b * c.Hkv;
-        const int64_t n = before[b + 1] - before[b], begin = first_of(b) + h * n;
-        const unsigned int others =
-            static_cast<unsigned int>(cta_of(begin + n - 1) - cta_of(begin));
-        const bool last = atomicAdd(tickets + pair, 1u) == others;
-        last_s[tid] = last;
+        __threadfence();  // (for the whole CTA, which has met at the barrier)
+        const int pair = tid == 0 ? slot0_pair : slot1_pair, b = pair / c.Hkv, h = pair - b * c.Hkv;
+        const unsigned int arrived = atomicAdd(tickets + pair, 1u);
+        const int64_t n = tiles_before(b + 1) - tiles_before(b), begin = first_of(b) + h * n;
+        const int c0 = cta_of(b, h, n, 0), n_parts = cta_of(b, h, n, n - 1) - c0 + 1;
+        // CTA c0 holds the pair in its last slot: the second one if a pair
+        // that begins before the CTA takes the first
+        bool second = false;
+        const int64_t clo = tile_from(total * c0 / n_ctas);
+        if (clo < begin) {
+            const int rb = row_at(clo);
+            second = (clo - first_of(rb)) % (tiles_before(rb + 1) - tiles_before(rb)) != 0;
+        }
+        const bool last = arrived == static_cast<unsigned int>(n_parts - 1);
+        join_s[tid] = make_int3(last ? n_parts : 0, c0, second);
         if (last) tickets[pair] = 0;  // ready for the next call
+        __threadfence();
     }
     __syncthreads();
     for (int k = 0; k < n_slots; ++k) {
-        if (!last_s[k]) continue;
-        __threadfence();
-        const int pair = slot_pair[k], b = pair / c.Hkv, h = pair - b * c.Hkv;
-        const int64_t n = before[b + 1] - before[b], begin = first_of(b) + h * n;
-        const int c0 = static_cast<int>(cta_of(begin)), c1 = static_cast<int>(cta_of(begin + n - 1));
-        // CTA c0 holds the pair in its last slot: the second one if its
-        // first is taken by a pair that began before it
-        auto slot = [&](int cta) {
-            if (cta > c0) return static_cast<int64_t>(cta) * 2;
-            const int64_t clo = total * c0 / n_ctas;
-            const int rb = row_at(clo);
-            const int64_t rn = before[rb + 1] - before[rb], off = clo - first_of(rb);
-            const int64_t pb = first_of(rb) + off / rn * rn;  // the pair at its first tile
-            const bool open = pb < clo;                       // begins before it
-            return static_cast<int64_t>(cta) * 2 + (open && pb != begin ? 1 : 0);
-        };
-        const int64_t slot0 = slot(c0);
-        for (int i = tid; i < r * D; i += THREADS) {
-            const int row = i / D;
-            float mx = -INFINITY, sum = 0.f, acc = 0.f;
-            for (int y = c0; y <= c1; ++y) {
-                const float *p = part + (y == c0 ? slot0 : static_cast<int64_t>(y) * 2) * PS;
-                mx = fmaxf(mx, __ldcg(p + r * D + row));
+        const int n_parts = join_s[k].x;
+        if (n_parts == 0) continue;
+        const int pair = k == 0 ? slot0_pair : slot1_pair, b = pair / c.Hkv, h = pair - b * c.Hkv;
+        const float *p0 = part + static_cast<int64_t>(join_s[k].y) * 2 * PS;
+        const int skip0 = join_s[k].z ? PS : 0;
+        auto part_at = [&](int y) { return p0 + (y == 0 ? skip0 : y * 2 * PS); };
+        // A thread for 4 dims of a head, and as many threads for those as
+        // there are, each with parts of its own, 8 asked for at once.
+        const int cols = r * D / 4, groups = max(1, kThreads / cols);
+        const int grp = tid / min(cols, kThreads);
+        float4 *red = reinterpret_cast<float4 *>(smem);               // [kThreads]
+        float2 *red_ml = reinterpret_cast<float2 *>(red + kThreads);  // [kThreads]
+        for (int i = tid - grp * cols; i < cols; i += kThreads) {
+            const int q = i / (D / 4);
+            float mx = -INFINITY, sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            auto add = [&](float m2, float l2, float4 v) {
+                const float to = fmaxf(mx, m2), use = to == -INFINITY ? 0.f : to;
+                const float f = fast_exp2(mx - use), f2 = fast_exp2(m2 - use);
+                mx = to;
+                sum = fmaf(sum, f, l2 * f2);
+                acc.x = fmaf(acc.x, f, v.x * f2);
+                acc.y = fmaf(acc.y, f, v.y * f2);
+                acc.z = fmaf(acc.z, f, v.z * f2);
+                acc.w = fmaf(acc.w, f, v.w * f2);
+            };
+            for (int y0 = grp; grp < groups && y0 < n_parts; y0 += 8 * groups) {
+                float m8[8], l8[8];
+                float4 v8[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int y = y0 + u * groups;
+                    m8[u] = -INFINITY;
+                    l8[u] = 0.f;
+                    v8[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (y < n_parts) {
+                        const float *p = part_at(y);
+                        m8[u] = __ldcg(p + r * D + q);
+                        l8[u] = __ldcg(p + r * D + r + q);
+                        v8[u] = __ldcg(reinterpret_cast<const float4 *>(p) + i);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) add(m8[u], l8[u], v8[u]);
             }
-            const float use = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 4
-            for (int y = c0; y <= c1; ++y) {
-                const float *p = part + (y == c0 ? slot0 : static_cast<int64_t>(y) * 2) * PS;
-                const float f = fast_exp2(__ldcg(p + r * D + row) - use);
-                sum = fmaf(f, __ldcg(p + r * D + r + row), sum);
-                acc = fmaf(f, __ldcg(p + i), acc);
+            if (groups > 1) {  // (one round: cols < kThreads)
+                red[tid] = acc;
+                red_ml[tid] = make_float2(mx, sum);
+                __syncthreads();
+                for (int y = 1; grp == 0 && y < groups; ++y)
+                    add(red_ml[y * cols + i].x, red_ml[y * cols + i].y, red[y * cols + i]);
             }
-            put((static_cast<int64_t>(b) * c.Hq + h * r) * D + i, sum > 0.f ? acc / sum : 0.f);
+            if (grp == 0) {
+                const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+                put4(o_t, o_f32, (static_cast<int64_t>(b) * c.Hq + h * r) * D + i * 4,
+                     make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+            }
         }
+        __syncthreads();  // shared memory is used again
     }
 }
 
@@ -658,7 +949,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 
 size_t paged_decode_part_bytes(const cca_paged_cache &c)
 {
-    return sizeof(float) * 2 * kCtas * (c.Hq / c.Hkv) * (c.d + 2);
+    return sizeof(float) * 2 * kCtas * part_floats(c.d, c.Hq / c.Hkv);
 }
 
 cudaError_t launch_paged_decode(const cca_paged_cache &c, int layer, const void *q_t,
@@ -670,34 +961,46 @@ cudaError_t launch_paged_decode(const cca_paged_cache &c, int layer, const void 
     const int r = c.Hq / c.Hkv;
     const PagedView v = paged_view(c, layer);
     const float scale_log2 = kLog2e / sqrtf(static_cast<float>(c.d));
-    auto smem_of = [&](int warps) {
-        return sizeof(float) * ((warps * warp_floats(c.d, r, c.g) + 1) / 2 * 2) +
-               sizeof(int64_t) * (c.B + 1);
-    };
-    auto go = [&](auto kern, int warps) {
+    auto go = [&](auto kern, int warps, int stages) {
+        const size_t smem = decode_smem(c.d, r, warps, stages, c.B);
         const cudaError_t e = cudaFuncSetAttribute(
-            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_of(warps)));
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
-        kern<<<kCtas, warps * 32, smem_of(warps), s>>>(
+        kern<<<kCtas, warps * 32, smem, s>>>(
             v, static_cast<const uint16_t *>(q_t), static_cast<const uint16_t *>(k_t),
             static_cast<const uint16_t *>(v_t), o_t, o_f32 ? 1 : 0, scale_log2,
             reinterpret_cast<float *>(base + w.part),
             reinterpret_cast<unsigned int *>(base + w.tickets));
         return cudaGetLastError();
     };
-    auto pick = [&](auto d, auto warps) {
-        constexpr int D = decltype(d)::value, W = decltype(warps)::value;
-        if (k_t != nullptr)
-            return r > 8 ? go(paged_decode_kernel<D, W, true, true>, W)
-                         : go(paged_decode_kernel<D, W, false, true>, W);
-        return r > 8 ? go(paged_decode_kernel<D, W, true, false>, W)
-                     : go(paged_decode_kernel<D, W, false, false>, W);
+    auto run = [&](auto d, auto warps, auto stages, auto wide) {
+        constexpr int D = decltype(d)::value, W = decltype(warps)::value,
+                      S = decltype(stages)::value;
+        constexpr bool WIDE = decltype(wide)::value;
+        return k_t != nullptr ? go(paged_decode_kernel<D, W, S, WIDE, true>, W, S)
+                              : go(paged_decode_kernel<D, W, S, WIDE, false>, W, S);
+    };
+    auto fits = [&](int warps, int stages) {  // in 227 KB, about 1 KB of them the kernel's own
+        return decode_smem(c.d, r, warps, stages, c.B) <= 227u * 1024u - 1100u;
     };
     using std::integral_constant;
-    if (c.d == 128) return pick(integral_constant<int, 128>{}, integral_constant<int, 8>{});
-    if (smem_of(16) <= 220u * 1024u)
-        return pick(integral_constant<int, 64>{}, integral_constant<int, 16>{});
-    return pick(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    const integral_constant<int, 128> d128{};
+    const integral_constant<int, 64> d64{};
+    const integral_constant<int, 12> n12{};
+    const integral_constant<int, 8> n8{};
+    const integral_constant<int, 3> n3{};
+    const integral_constant<int, 2> n2{};
+    const std::true_type wide{};
+    const std::false_type narrow{};
+    if (c.d == 128) {
+        if (r > 8) return run(d128, n8, n2, wide);
+        if (fits(12, 2)) return run(d128, n12, n2, narrow);
+        if (fits(8, 3)) return run(d128, n8, n3, narrow);
+        return run(d128, n8, n2, narrow);
+    }
+    if (r > 8) return run(d64, n8, n2, wide);
+    if (fits(12, 2)) return run(d64, n12, n2, narrow);
+    return run(d64, n8, n2, narrow);
 }
 
 cudaError_t paged_decode_status_read_clear(unsigned int *v)
