@@ -582,41 +582,56 @@ def cca_attn_decode_noalloc(cache: Cache, q_t, o_t=None, out_dtype=None, stream=
 
 # ---- packed prompts: sequences of different lengths without padding
 
-def _here(t, name: str):
-    """``t`` is a CUDA tensor of the current device (the library launches
-    on that one)."""
-    if not t.is_cuda:
+def _device(t, name: str) -> int:
+    """The device of a call's first tensor, which has to be the current one
+    (the library launches on that)."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != _torch().cuda.current_device():
+    if dev != _torch().cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return t
+    return dev
 
 
-def _tensor(t, name: str, shape, dtype):
+def _here(t, name: str, dev: int) -> int:
+    """Pointer of a tensor on the call's device."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor of device {dev}, is on {t.device}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    """The stream's handle; None: the current one (in a call of a few
+    microseconds, cheaper than a Stream object)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(dev)
+
+
+def _tensor(t, name: str, shape, dtype, dev: int) -> int:
     """Pointer of a contiguous tensor of this shape on the current device."""
     if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)}")
-    return ctypes.c_void_p(_here(t, name).data_ptr())
+    return _here(t, name, dev)
 
 
-def _rows(t, name: str, shape, dtype=None):
+def _rows(t, name: str, shape, dtype, dev: int):
     """A [heads, total, d] tensor of any row and head strides as the
     library's packed tensor."""
-    want = dtype or _torch().bfloat16
-    if t.dtype != want or t.shape != shape:
-        raise ValueError(f"{name} must be a {want} tensor {tuple(shape)}, got "
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)}")
     head, row, one = t.stride()
     if one != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
-    return _RowsStruct(_here(t, name).data_ptr(), row, head)
+    return _RowsStruct(_here(t, name, dev), row, head)
 
 
-def _offsets(cu, name: str = "cu"):
-    if cu.dtype != _torch().int32 or cu.dim() != 1 or cu.numel() < 2 or not cu.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of S + 1 offsets")
-    return ctypes.c_void_p(_here(cu, name).data_ptr())
+def _offsets(cu, dev: int) -> int:
+    if cu.dtype != _torch().int32 or cu.dim() != 1 or cu.shape[0] < 2 or not cu.is_contiguous():
+        raise ValueError("cu must be a contiguous int32 tensor of S + 1 offsets")
+    return _here(cu, "cu", dev)
 
 
 def _packed_shapes(Q, K):
@@ -635,17 +650,19 @@ def cca_pool_packed(Q, K, V, cu, g: int, Kc=None, Vc=None, stream=None):
     start at row cu[s] // g, rows without a group are zero.
     """
     torch = _torch()
+    bf, dev = torch.bfloat16, _device(Q, "Q")
     Hq, Hkv, total, d = _packed_shapes(Q, K)
     shape = (Hkv, total // int(g) if g > 0 else 0, d)
     if Kc is None:
-        Kc = torch.empty(shape, dtype=torch.float16, device=Q.device)
+        Kc = Q.new_empty(shape, dtype=torch.float16)
     if Vc is None:
-        Vc = torch.empty(shape, dtype=torch.float16, device=Q.device)
+        Vc = Q.new_empty(shape, dtype=torch.float16)
     _check(lib().cca_pool_packed(
-        _rows(Q, "Q", (Hq, total, d)), _rows(K, "K", (Hkv, total, d)),
-        _rows(V, "V", (Hkv, total, d)), _offsets(cu), _tensor(Kc, "Kc", shape, torch.float16),
-        _tensor(Vc, "Vc", shape, torch.float16), cu.numel() - 1, Hq, Hkv, total, d, int(g),
-        _stream(stream)), "cca_pool_packed")
+        _rows(Q, "Q", (Hq, total, d), bf, dev), _rows(K, "K", (Hkv, total, d), bf, dev),
+        _rows(V, "V", (Hkv, total, d), bf, dev), _offsets(cu, dev),
+        _tensor(Kc, "Kc", shape, torch.float16, dev), _tensor(Vc, "Vc", shape, torch.float16, dev),
+        cu.shape[0] - 1, Hq, Hkv, total, d, int(g),
+        _raw_stream(stream, dev)), "cca_pool_packed")
     return Kc, Vc
 
 
@@ -662,28 +679,31 @@ def cca_attn_prefill_packed(Q, K, V, Kc, Vc, cu, g: int, w: int, O=None, out_dty
     no sequence are not written.
     """
     torch = _torch()
+    bf, dev = torch.bfloat16, _device(Q, "Q")
     Hq, Hkv, total, d = _packed_shapes(Q, K)
-    S = cu.numel() - 1
+    S = cu.shape[0] - 1
     if O is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
-        if Q.stride(0) < Q.stride(1):  # [total, Hq, d] in memory
-            O = torch.empty((total, Hq, d), dtype=dt, device=Q.device).transpose(0, 1)
+        if Q.is_contiguous():
+            O = Q.new_empty((Hq, total, d), dtype=dt)
+        elif Q.stride(0) < Q.stride(1):  # [total, Hq, d] in memory
+            O = Q.new_empty((total, Hq, d), dtype=dt).transpose(0, 1)
         else:
-            O = torch.empty((Hq, total, d), dtype=dt, device=Q.device)
+            O = Q.new_empty((Hq, total, d), dtype=dt)
     if workspace is None:
-        workspace = torch.empty(max(cca_packed_workspace_bytes(S, total), 256),
-                                dtype=torch.uint8, device=Q.device)
+        workspace = Q.new_empty(max(cca_packed_workspace_bytes(S, total), 256),
+                                dtype=torch.uint8)
         if stream is not None:  # freed on return: not before the work on that stream is done
             workspace.record_stream(stream)
     core = (Hkv, total // int(g) if g > 0 else 0, d)
     _check(lib().cca_attn_prefill_packed(
-        _rows(Q, "Q", (Hq, total, d)), _rows(K, "K", (Hkv, total, d)),
-        _rows(V, "V", (Hkv, total, d)),
-        None if Kc is None else _tensor(Kc, "Kc", core, torch.float16),
-        None if Vc is None else _tensor(Vc, "Vc", core, torch.float16), _offsets(cu),
-        _rows(O, "O", (Hq, total, d), O.dtype), _odtype(O.dtype), S, Hq, Hkv, total, d, int(g),
-        int(w), ctypes.c_void_p(_here(workspace, "workspace").data_ptr()), workspace.numel(),
-        _stream(stream)), "cca_attn_prefill_packed")
+        _rows(Q, "Q", (Hq, total, d), bf, dev), _rows(K, "K", (Hkv, total, d), bf, dev),
+        _rows(V, "V", (Hkv, total, d), bf, dev),
+        None if Kc is None else _tensor(Kc, "Kc", core, torch.float16, dev),
+        None if Vc is None else _tensor(Vc, "Vc", core, torch.float16, dev), _offsets(cu, dev),
+        _rows(O, "O", (Hq, total, d), O.dtype, dev), _odtype(O.dtype), S, Hq, Hkv, total, d, int(g),
+        int(w), _here(workspace, "workspace", dev), workspace.numel(),
+        _raw_stream(stream, dev)), "cca_attn_prefill_packed")
     return O
 
 
@@ -742,6 +762,8 @@ class PagedCache:
         # zero-filled once, as the library asks for
         self.workspace = torch.zeros(max(cca_paged_workspace_bytes(self), 256),
                                      dtype=torch.uint8, device=device)
+        self.workspace_at = self.workspace.data_ptr(), self.workspace.numel()
+        self.q_shape, self.kv_shape = (B, int(Hq), d), (B, Hkv, d)
 
     @classmethod
     def from_tensors(cls, core_table, raw_table, core_ref, raw_ref, lens, k_core, v_core, k_raw,
@@ -802,28 +824,22 @@ def cca_paged_workspace_bytes(cache: PagedCache) -> int:
     return int(lib().cca_paged_workspace_bytes(ctypes.byref(cache.struct)))
 
 
-def _paged(cache: PagedCache):
-    """The cache's struct, once its buffers are known to be on the current
-    device."""
-    _here(cache.tables, "cache")
-    return ctypes.byref(cache.struct)
-
-
-def _paged_workspace(cache: PagedCache, workspace):
-    ws = cache.workspace if workspace is None else _here(workspace, "workspace")
-    return ctypes.c_void_p(ws.data_ptr()), ws.numel()
+def _paged_workspace(cache: PagedCache, workspace, dev: int):
+    if workspace is None:  # (on the cache's device)
+        return cache.workspace_at
+    return _here(workspace, "workspace", dev), workspace.numel()
 
 
 def cca_paged_reserve(cache: PagedCache, n, stream=None) -> None:
     """Lengthen rows and give them the pages of their new tokens: ``n`` is a
     number of tokens for every row that is not free, or an int64 CUDA tensor
     [B] of each row's.  Raw pages before the new window are given back."""
-    torch = _torch()
+    torch, dev = _torch(), _device(cache.tables, "cache")
     if isinstance(n, torch.Tensor):
-        each, n = _tensor(n, "n", (cache.B,), torch.int64), 0
+        each, n = _tensor(n, "n", (cache.B,), torch.int64, dev), 0
     else:
         each = None
-    _check(lib().cca_paged_reserve(_paged(cache), each, int(n), _stream(stream)),
+    _check(lib().cca_paged_reserve(cache.struct, each, int(n), _raw_stream(stream, dev)),
            "cca_paged_reserve")
 
 
@@ -833,31 +849,31 @@ def cca_paged_fill(cache: PagedCache, K, V, Kc, Vc, cu, rows, layer: int = 0,
     their core rows Kc/Vc (cca_pool_packed; None without core pages):
     sequence s becomes row rows[s] (int32, CUDA, [S]), which
     cca_paged_reserve has given the sequence's length."""
-    torch = _torch()
+    torch, dev = _torch(), _device(cache.tables, "cache")
     total = K.shape[1]
-    S = cu.numel() - 1
-    core = (cache.Hkv, total // cache.g, cache.d)
+    S = cu.shape[0] - 1
+    shape, core = (cache.Hkv, total, cache.d), (cache.Hkv, total // cache.g, cache.d)
     _check(lib().cca_paged_fill(
-        _paged(cache), int(layer), _rows(K, "K", (cache.Hkv, total, cache.d)),
-        _rows(V, "V", (cache.Hkv, total, cache.d)),
-        None if Kc is None else _tensor(Kc, "Kc", core, torch.float16),
-        None if Vc is None else _tensor(Vc, "Vc", core, torch.float16), _offsets(cu),
-        _tensor(rows, "rows", (S,), torch.int32), S, total, _stream(stream)), "cca_paged_fill")
+        cache.struct, int(layer), _rows(K, "K", shape, torch.bfloat16, dev),
+        _rows(V, "V", shape, torch.bfloat16, dev),
+        None if Kc is None else _tensor(Kc, "Kc", core, torch.float16, dev),
+        None if Vc is None else _tensor(Vc, "Vc", core, torch.float16, dev), _offsets(cu, dev),
+        _tensor(rows, "rows", (S,), torch.int32, dev), S, total, _raw_stream(stream, dev)),
+        "cca_paged_fill")
 
 
 def cca_attn_decode_paged(cache: PagedCache, q_t, layer: int = 0, o_t=None, out_dtype=None,
                           workspace=None, stream=None):
     """Attention of the newest token of every row: q_t [B,Hq,d] -> o_t
     [B,Hq,d]; free rows get zeros.  Capturable in a CUDA graph."""
-    torch = _torch()
-    shape = (cache.B, cache.Hq, cache.d)
+    torch, dev = _torch(), _device(cache.tables, "cache")
+    shape = cache.q_shape
     if o_t is None:
-        o_t = torch.empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype,
-                          device=q_t.device)
+        o_t = q_t.new_empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
     _check(lib().cca_attn_decode_paged(
-        _paged(cache), int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16),
-        _tensor(o_t, "o_t", shape, o_t.dtype), _odtype(o_t.dtype),
-        *_paged_workspace(cache, workspace), _stream(stream)), "cca_attn_decode_paged")
+        cache.struct, int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16, dev),
+        _tensor(o_t, "o_t", shape, o_t.dtype, dev), _odtype(o_t.dtype),
+        *_paged_workspace(cache, workspace, dev), _raw_stream(stream, dev)), "cca_attn_decode_paged")
     return o_t
 
 
@@ -867,16 +883,15 @@ def cca_paged_step(cache: PagedCache, q_t, k_t, v_t, layer: int = 0, o_t=None, o
     every row (q_t [B,Hq,d], k_t/v_t [B,Hkv,d]; cca_paged_reserve(cache, 1)
     has made room for it, once for all layers) and return its attention
     output o_t [B,Hq,d].  Capturable in a CUDA graph."""
-    torch = _torch()
-    shape, kv = (cache.B, cache.Hq, cache.d), (cache.B, cache.Hkv, cache.d)
+    torch, dev = _torch(), _device(cache.tables, "cache")
+    shape, kv = cache.q_shape, cache.kv_shape
     if o_t is None:
-        o_t = torch.empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype,
-                          device=q_t.device)
+        o_t = q_t.new_empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
     _check(lib().cca_paged_step(
-        _paged(cache), int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16),
-        _tensor(k_t, "k_t", kv, torch.bfloat16), _tensor(v_t, "v_t", kv, torch.bfloat16),
-        _tensor(o_t, "o_t", shape, o_t.dtype), _odtype(o_t.dtype),
-        *_paged_workspace(cache, workspace), _stream(stream)), "cca_paged_step")
+        cache.struct, int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16, dev),
+        _tensor(k_t, "k_t", kv, torch.bfloat16, dev), _tensor(v_t, "v_t", kv, torch.bfloat16, dev),
+        _tensor(o_t, "o_t", shape, o_t.dtype, dev), _odtype(o_t.dtype),
+        *_paged_workspace(cache, workspace, dev), _raw_stream(stream, dev)), "cca_paged_step")
     return o_t
 
 
@@ -885,22 +900,22 @@ def cca_paged_fork(cache: PagedCache, parent, workspace=None, stream=None) -> No
     -1: frees it), for all layers.  Full pages are shared, partly filled last
     ones copied: samples of one prompt, beams that change places, rows that
     are done."""
-    torch = _torch()
+    torch, dev = _torch(), _device(cache.tables, "cache")
     _check(lib().cca_paged_fork(
-        _paged(cache), _tensor(parent, "parent", (cache.B,), torch.int32),
-        *_paged_workspace(cache, workspace), _stream(stream)), "cca_paged_fork")
+        cache.struct, _tensor(parent, "parent", (cache.B,), torch.int32, dev),
+        *_paged_workspace(cache, workspace, dev), _raw_stream(stream, dev)), "cca_paged_fork")
 
 
 def cca_paged_compact(cache: PagedCache, live=None, workspace=None, stream=None):
     """Move the pages in use to the front of their pools, for all layers.
     Returns ``live`` (int64, CUDA, [2]): pages in use of the core and of the
     raw pool."""
-    torch = _torch()
+    torch, dev = _torch(), _device(cache.tables, "cache")
     if live is None:
-        live = torch.empty(2, dtype=torch.int64, device=cache.tables.device)
+        live = cache.tables.new_empty(2, dtype=torch.int64)
     _check(lib().cca_paged_compact(
-        _paged(cache), _tensor(live, "live", (2,), torch.int64),
-        *_paged_workspace(cache, workspace), _stream(stream)), "cca_paged_compact")
+        cache.struct, _tensor(live, "live", (2,), torch.int64, dev),
+        *_paged_workspace(cache, workspace, dev), _raw_stream(stream, dev)), "cca_paged_compact")
     return live
 
 

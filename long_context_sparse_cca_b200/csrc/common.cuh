@@ -87,6 +87,15 @@ __device__ __forceinline__ uint4 ldg_stream(const void *p)
     return v;
 }
 
+// First thing in a kernel that launch_chained launches: waits until the
+// kernel before it in the stream has ended and its writes are visible, and
+// lets the next one be set up.
+__device__ __forceinline__ void chain_begin()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll

@@ -66,6 +66,25 @@ cudaError_t launch_prefill(const void *Q, const void *K, const void *V,
                            int B, int Hq, int Hkv, int64_t T, int d, int g,
                            int w, cudaStream_t s, float *lse = nullptr);
 
+// Launch a kernel that begins with chain_begin() (common.cuh): its blocks
+// may be set up while the kernel before it in the stream still runs.
+template <class... P, class... A>
+cudaError_t launch_chained(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                           A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // Packed sequences: one packed tensor (element strides of a row and of a
 // head), the list of their 256-row query blocks (most key tiles first), and
 // the calls of the packed prompts.

@@ -15,20 +15,13 @@ namespace {
 constexpr int kPlanThreads = 256;
 constexpr int kPoolWarps = 8;
 
-// The attention kernel takes (sequence, 256-row block) pairs with the most
-// key tiles first, so that the last ones to finish are short.  A block's
-// number within its sequence orders them (window and core rows only grow
-// with it): block `blk` of sequence s comes after every block of a higher
-// number and after the same block of the sequences before s.  Each thread
-// takes one pair and counts those before it; the pairs are found from the
-// offsets alone, at cu[s] / 256 + s + blk (a sequence of n rows has at most
-// cu[s + 1] / 256 - cu[s] / 256 + 1 blocks, so no two pairs meet; places
-// that hold none are skipped).
+// The list of the attention kernel's query blocks (packed.cuh).
 __global__ void __launch_bounds__(kPlanThreads)
     packed_plan_kernel(const int *__restrict__ cu, int S, int64_t total, int g,
                        int4 *__restrict__ blocks, int *__restrict__ count)
 {
     extern __shared__ int scu[];  // [S + 1] offsets
+    chain_begin();
     if (!load_offsets(cu, S, total, scu)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) {
             *count = 0;
@@ -36,11 +29,10 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         return;
     }
-    auto blocks_of = [&](int s) { return (scu[s + 1] - scu[s] + 255) >> 8; };
     if (blockIdx.x == 0) {
         __shared__ int warp_sum_s[kPlanThreads / 32];
         int n = 0;
-        for (int s = threadIdx.x; s < S; s += kPlanThreads) n += blocks_of(s);
+        for (int s = threadIdx.x; s < S; s += kPlanThreads) n += packed_blocks(scu, s);
         n = __reduce_add_sync(0xffffffffu, n);
         if ((threadIdx.x & 31) == 0) warp_sum_s[threadIdx.x >> 5] = n;
         __syncthreads();
@@ -52,36 +44,27 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     const int64_t i = static_cast<int64_t>(blockIdx.x) * kPlanThreads + threadIdx.x;
     if (i >= total / 256 + S) return;
-    // the last sequence whose first place is not behind i
-    int lo = 0, hi = S - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if ((scu[mid] >> 8) + static_cast<int64_t>(mid) <= i)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    const int64_t b64 = i - ((scu[lo] >> 8) + static_cast<int64_t>(lo));
-    if (b64 < 0 || b64 >= blocks_of(lo)) return;
-    const int blk = static_cast<int>(b64);
-    int place = 0;
-    for (int s = 0; s < S; ++s) {
-        const int n = blocks_of(s);
-        place += max(0, n - blk - 1) + (s < lo && n > blk ? 1 : 0);
-    }
-    blocks[place] = make_int4(scu[lo], scu[lo + 1] - scu[lo], blk, scu[lo] / g);
+    const PackedPair pair = packed_pair(scu, S, i);
+    if (pair.blk < 0) return;
+    const int first = scu[pair.s];
+    blocks[packed_place(scu, S, pair)] =
+        make_int4(first, scu[pair.s + 1] - first, pair.blk, first / g);
 }
 
 // As pool_kernel (pool.cu), one warp per (head, core row): the core row's
 // sequence is the last one whose first core row cu[s] / g is not behind it.
 // Rows that hold no group become zero.
+// Three blocks fit an SM where the group's keys take up to 32 registers of
+// a thread and its values are loaded only after them: 32K tokens of 32 heads
+// take 125 us instead of 137 with two (D = 128, G = 32 would spill).
 template <int D, int G>
-__global__ void __launch_bounds__(kPoolWarps * 32, 2)
+__global__ void __launch_bounds__(kPoolWarps * 32, G > 0 && D * G <= 2048 ? 3 : 2)
     pool_packed_kernel(PackedRows Q, PackedRows K, PackedRows V, const int *__restrict__ cu,
                        uint16_t *__restrict__ Kc, uint16_t *__restrict__ Vc, int S, int Hkv, int r,
                        int64_t total, int g, int64_t m, float scale_log2)
 {
     extern __shared__ int scu[];  // [S + 1] offsets, then the warps' scratch
+    chain_begin();
     if (!load_offsets(cu, S, total, scu)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_packed_status, kStatusSeqlens);
         return;
@@ -92,30 +75,49 @@ __global__ void __launch_bounds__(kPoolWarps * 32, 2)
     const auto *k = static_cast<const uint16_t *>(K.data);
     const auto *v = static_cast<const uint16_t *>(V.data);
     const int64_t n = static_cast<int64_t>(Hkv) * m;
-    for (int64_t gid = static_cast<int64_t>(blockIdx.x) * kPoolWarps + warp; gid < n;
-         gid += static_cast<int64_t>(gridDim.x) * kPoolWarps) {
-        const int64_t h = gid / m;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kPoolWarps;
+    // first token of group gid = h m + c (-1: none) and its head
+    auto place = [&](int64_t gid, int &h) {
+        h = static_cast<int>(gid / m);
         const int c = static_cast<int>(gid - h * m);
         const int s = core_row_sequence(scu, S, g, c);
         const int j = c - scu[s] / g;
+        return j < 0 || j >= (scu[s + 1] - scu[s]) / g ? -1 : scu[s] + j * g;
+    };
+    int64_t gid = static_cast<int64_t>(blockIdx.x) * kPoolWarps + warp;
+    int h_next = 0, next = gid < n ? place(gid, h_next) : -1;
+    for (; gid < n; gid += step) {
+        const int64_t first = next;
+        const int h = h_next;
+        if (gid + step < n) {
+            // the next group's rows on their way to L2 while this one is pooled
+            next = place(gid + step, h_next);
+            constexpr int LINES = D / 64;  // 128-byte lines of a row
+            if (next >= 0)
+                for (int i = lane; i < g * LINES; i += 32) {
+                    const int64_t row = next + i / LINES;
+                    const int e = i % LINES * 64;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(k + h_next * K.head + row * K.row + e));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(v + h_next * V.head + row * V.row + e));
+                }
+        }
         uint16_t *kc = Kc + gid * D, *vc = Vc + gid * D;
-        if (j < 0 || j >= (scu[s + 1] - scu[s]) / g) {
+        if (first < 0) {
             if (lane < D / 8) {
                 reinterpret_cast<uint4 *>(kc)[lane] = make_uint4(0u, 0u, 0u, 0u);
                 reinterpret_cast<uint4 *>(vc)[lane] = make_uint4(0u, 0u, 0u, 0u);
             }
             continue;
         }
-        const int64_t first = scu[s] + static_cast<int64_t>(j) * g;
         const uint16_t *Kg = k + h * K.head + first * K.row;
         const uint16_t *Vg = v + h * V.head + first * V.row;
-        const uint16_t *Qb = q + h * r * Q.head + (first + g - 1) * Q.row;
+        const uint16_t *Qb = q + static_cast<int64_t>(h) * r * Q.head + (first + g - 1) * Q.row;
         auto krow = [&](int i) { return Kg + i * K.row; };
         auto vrow = [&](int i) { return Vg + i * V.row; };
         auto qrow = [&](int i) { return Qb + i * Q.head; };
         bool over;
         if constexpr (G > 0)
-            over = pool_group_warp_fast<D, G>(krow, vrow, qrow, r, scale_log2, scratch, kc, vc);
+            over = pool_group_warp_fast<D, G, false>(krow, vrow, qrow, r, scale_log2, scratch, kc, vc);
         else
             over = pool_group_warp<D>(krow, vrow, qrow, r, g, scale_log2, scratch, kc, vc);
         if (over && lane == 0) atomicOr(&g_packed_status, kStatusRange);
@@ -130,9 +132,8 @@ cudaError_t launch_packed_plan(const int *cu, int S, int64_t total, int g, int4 
 {
     const int64_t n = packed_max_blocks(S, total);
     const int grid = static_cast<int>((n + kPlanThreads - 1) / kPlanThreads);
-    packed_plan_kernel<<<grid, kPlanThreads, sizeof(int) * (S + 1), s>>>(cu, S, total, g,
-                                                                         blocks, count);
-    return cudaGetLastError();
+    return launch_chained(packed_plan_kernel, grid, kPlanThreads, sizeof(int) * (S + 1), s, cu, S,
+                          total, g, blocks, count);
 }
 
 size_t pool_packed_smem(int S, int r, int g)
@@ -151,7 +152,8 @@ cudaError_t launch_pool_packed(const PackedRows &Q, const PackedRows &K, const P
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     const int64_t want = (n + kPoolWarps - 1) / kPoolWarps;
-    const int blocks = static_cast<int>(want < 64LL * sms ? want : 64LL * sms);
+    // few enough that a block's offsets are loaded for many groups
+    const int blocks = static_cast<int>(want < 8LL * sms ? want : 8LL * sms);
     const float scale_log2 = kLog2e / sqrtf(static_cast<float>(d));
     cudaError_t e = cudaSuccess;
     auto go = [&](auto kern) {
@@ -159,10 +161,9 @@ cudaError_t launch_pool_packed(const PackedRows &Q, const PackedRows &K, const P
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(smem));
         if (e != cudaSuccess) return;
-        kern<<<blocks, kPoolWarps * 32, smem, s>>>(Q, K, V, cu, static_cast<uint16_t *>(Kc),
-                                                    static_cast<uint16_t *>(Vc), S, Hkv, r, total,
-                                                    g, m, scale_log2);
-        e = cudaGetLastError();
+        e = launch_chained(kern, blocks, kPoolWarps * 32, smem, s, Q, K, V, cu,
+                           static_cast<uint16_t *>(Kc), static_cast<uint16_t *>(Vc), S, Hkv, r,
+                           total, g, m, scale_log2);
     };
     if (d == 128) {
         if (g == 16)

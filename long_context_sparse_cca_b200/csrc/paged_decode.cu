@@ -191,6 +191,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     __shared__ int pools_s[kWarps];
     __shared__ int3 join_s[2];  // parts to join (0: not here), CTA of the first, its slot
 
+    chain_begin();
     if (tid < 2 * kWarps) ids[tid] = -1;
     {  // the list: each thread sums its rows, then a scan over the block
         const int per = (c.B + kThreads - 1) / kThreads;
@@ -966,12 +967,11 @@ cudaError_t launch_paged_decode(const cca_paged_cache &c, int layer, const void 
         const cudaError_t e = cudaFuncSetAttribute(
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
-        kern<<<kCtas, warps * 32, smem, s>>>(
-            v, static_cast<const uint16_t *>(q_t), static_cast<const uint16_t *>(k_t),
-            static_cast<const uint16_t *>(v_t), o_t, o_f32 ? 1 : 0, scale_log2,
-            reinterpret_cast<float *>(base + w.part),
-            reinterpret_cast<unsigned int *>(base + w.tickets));
-        return cudaGetLastError();
+        return launch_chained(kern, kCtas, warps * 32, smem, s, v, static_cast<const uint16_t *>(q_t),
+                              static_cast<const uint16_t *>(k_t),
+                              static_cast<const uint16_t *>(v_t), o_t, o_f32 ? 1 : 0, scale_log2,
+                              reinterpret_cast<float *>(base + w.part),
+                              reinterpret_cast<unsigned int *>(base + w.tickets));
     };
     auto run = [&](auto d, auto warps, auto stages, auto wide) {
         constexpr int D = decltype(d)::value, W = decltype(warps)::value,

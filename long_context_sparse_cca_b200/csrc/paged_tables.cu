@@ -20,7 +20,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kScanThreads = 1024;
+constexpr int kThreads = 512;         // of the kernels that plan
+constexpr int kChunk = 4 * kThreads;  // pages that a block looks at at once
 
 struct Pool {  // one of the two pools' tables
     int *table, *ref;
@@ -35,122 +36,144 @@ struct TablesView {
 
 __device__ __forceinline__ void report(unsigned int bits) { atomicOr(&g_paged_tables_status, bits); }
 
-// Exclusive sum over the block of each thread's x (kScanThreads threads);
-// `total`: the sum of all.  Called by every thread, any number of times.
-__device__ __forceinline__ int block_scan(int x, int &total)
+// Exclusive sums over the block (kThreads threads) of each thread's x;
+// total: the sums of all.  One barrier; `room` is used again only after
+// another one.
+template <int N, class T>
+__device__ __forceinline__ void block_scan(T (&x)[N], T (&total)[N], T (&room)[kThreads / 32][N])
 {
-    __shared__ int warp_sums[kScanThreads / 32];
+    constexpr int W = kThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int y = x;
+    T in[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-    }
-    if (lane == 31) warp_sums[warp] = y;
-    __syncthreads();
-    if (warp == 0) {
-        int v = warp_sums[lane];
+    for (int i = 0; i < N; ++i) {
+        in[i] = x[i];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int z = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += z;
+            const T y = __shfl_up_sync(0xffffffffu, x[i], o);
+            if (lane >= o) x[i] += y;
         }
-        warp_sums[lane] = v;
+        if (lane == 31) room[warp][i] = x[i];
     }
     __syncthreads();
-    const int before = warp > 0 ? warp_sums[warp - 1] : 0;
-    total = warp_sums[kScanThreads / 32 - 1];
-    __syncthreads();
-    return before + y - x;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        T y = lane < W ? room[lane][i] : T(0);
+#pragma unroll
+        for (int o = 1; o < W; o <<= 1) {
+            const T z = __shfl_up_sync(0xffffffffu, y, o);
+            if (lane >= o) y += z;
+        }
+        total[i] = __shfl_sync(0xffffffffu, y, W - 1);
+        const T before = __shfl_sync(0xffffffffu, y, warp > 0 ? warp - 1 : 0);
+        x[i] += (warp > 0 ? before : T(0)) - in[i];
+    }
 }
 
-// Free pages of a pool, by the whole block.
-__device__ __forceinline__ int count_free(const int *ref, int pages)
+// Free pages among this thread's four of a chunk, a bit for each.
+__device__ __forceinline__ int free_bits(const int *ref, int pages, int chunk)
 {
-    int n = 0;
-    for (int p = threadIdx.x; p < pages; p += kScanThreads) n += __ldcg(ref + p) == 0;
-    int total;
-    block_scan(n, total);
-    return total;
+    int bits = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int p = chunk + threadIdx.x * 4 + u;
+        if (p < pages && __ldcg(ref + p) == 0) bits |= 1 << u;
+    }
+    return bits;
 }
 
-// use(k, page) for the k-th free page, k < want, by the whole block.
+// use(k, page) for this thread's free pages, the first of them the k-th, as
+// long as k < want.
 template <class F>
-__device__ __forceinline__ void take_free(const int *ref, int pages, int want, F use)
+__device__ __forceinline__ void use_free(int bits, int chunk, int k, int want, F use)
 {
-    for (int p0 = 0, base = 0; p0 < pages && base < want; p0 += kScanThreads) {
-        const int p = p0 + threadIdx.x;
-        const bool free = p < pages && __ldcg(ref + p) == 0;
-        int total;
-        const int k = base + block_scan(free ? 1 : 0, total);
-        if (free && k < want) use(k, p);
-        base += total;
-    }
+    for (int u = 0; u < 4; ++u)
+        if (bits >> u & 1) {
+            if (k < want) use(k, chunk + threadIdx.x * 4 + u);
+            ++k;
+        }
 }
 
 // cca_paged_reserve: a cluster of two blocks, one for each pool; both plan
-// all rows, then each takes its own pool's pages.
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScanThreads)
+// all rows, then each takes its own pool's pages.  Bound by the chain of
+// loads and barriers (a scan of everything at once, one exchange between the
+// blocks): 5 us for a few rows.
+struct Grow {
+    int64_t len, n;       // the row's length, the tokens it is given
+    bool refused;         // asked for what its table cannot take
+    int core, n_core;     // first column and number of its new pages
+    int raw, n_raw;
+    int gone, gone_end;   // raw columns that go
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
     reserve_kernel(TablesView v, const long long *__restrict__ n_new, long long n_all)
 {
-    extern __shared__ int plan[];  // [B + 1] my pool's pages wanted before row b, [B] granted
+    // of each row: wanted pages of my pool before it, [B], and the column of
+    // its first one (-1: nothing granted), [B]
+    extern __shared__ int plan[];
+    __shared__ int64_t rows_room[kThreads / 32][2];
+    __shared__ int free_room[kThreads / 32][2], chunk_room[2][kThreads / 32][1];
     __shared__ int free_pages;
+    chain_begin();
     cg::cluster_group cluster = cg::this_cluster();
     const int me = cluster.block_rank();
-    int *before = plan, *granted = plan + v.B + 1;
+    int *before = plan, *column = plan + v.B;
+    const Pool &pool = v.pool[me];
     const bool core = v.pool[0].cols > 0;
     const int64_t longest = paged_max_len(v.pool[1].cols, v.pool[0].cols, v.g, v.shift);
-    auto grow = [&](int b, int64_t &len) -> int64_t {
-        len = v.lens[b];
-        const int64_t n = n_new != nullptr ? n_new[b] : (len > 0 ? n_all : 0);
-        return n > 0 && len >= 0 && n <= longest - len ? n : 0;
+    auto grow = [&](int b) {
+        Grow r = {};
+        r.len = v.lens[b];
+        const int64_t n = n_new != nullptr ? n_new[b] : (r.len > 0 ? n_all : 0);
+        r.n = n > 0 && r.len >= 0 && n <= longest - r.len ? n : 0;
+        r.refused = r.n != n;
+        if (r.n == 0) return r;
+        const PagedCols a = paged_cols(r.len, v.g, v.w, v.shift, core);
+        const PagedCols z = paged_cols(r.len + r.n, v.g, v.w, v.shift, core);
+        r.core = a.core_hi;
+        r.n_core = z.core_hi - a.core_hi;
+        r.raw = max(a.raw_hi, z.raw_lo);
+        r.n_raw = z.raw_hi - r.raw;
+        r.gone = a.raw_lo;
+        r.gone_end = min(a.raw_hi, z.raw_lo);
+        return r;
     };
-    // pages that rows want: my pool's kept, the other's only for the decision
-    int want[2] = {0, 0};
-    const int per = (v.B + kScanThreads - 1) / kScanThreads;
-    const int b0 = threadIdx.x * per, b1 = min(b0 + per, v.B);
-    auto need = [&](int b, int (&x)[2]) {
-        int64_t len;
-        const int64_t n = grow(b, len);
-        x[0] = x[1] = 0;
-        if (n == 0) return;
-        const PagedCols a = paged_cols(len, v.g, v.w, v.shift, core);
-        const PagedCols z = paged_cols(len + n, v.g, v.w, v.shift, core);
-        x[0] = z.core_hi - a.core_hi;
-        x[1] = z.raw_hi - max(a.raw_hi, z.raw_lo);
-    };
+    const int per = (v.B + kThreads - 1) / kThreads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, v.B), b1 = min(b0 + per, v.B);
+    const int bits = free_bits(pool.ref, pool.pages, 0);
+    Grow first = {};
+    if (b0 < b1) first = grow(b0);
+    auto row_of = [&](int b) { return b == b0 ? first : grow(b); };
+    int64_t at[2] = {0, 0}, want[2];
     for (int b = b0; b < b1; ++b) {
-        int x[2];
-        need(b, x);
-        want[0] += x[0];
-        want[1] += x[1];
+        const Grow r = row_of(b);
+        at[0] += r.n_core;
+        at[1] += r.n_raw;
     }
-    int total[2], at[2];
-    at[0] = block_scan(want[0], total[0]);
-    at[1] = block_scan(want[1], total[1]);
-    const int n_free = total[me] > 0 ? count_free(v.pool[me].ref, v.pool[me].pages) : 0;
-    if (threadIdx.x == 0) free_pages = n_free;
+    int free_at[2] = {__popc(bits), 0}, free_all[2];  // in the first chunk, behind it
+    for (int chunk = kChunk; chunk < pool.pages; chunk += kChunk)
+        free_at[1] += __popc(free_bits(pool.ref, pool.pages, chunk));
+    block_scan(at, want, rows_room);
+    block_scan(free_at, free_all, free_room);
+    if (threadIdx.x == 0) free_pages = free_all[0] + free_all[1];
     cluster.sync();
     const int other = *cluster.map_shared_rank(&free_pages, me ^ 1);
-    const int have[2] = {me == 0 ? n_free : other, me == 0 ? other : n_free};
+    const int mine = free_all[0] + free_all[1];
+    const int have[2] = {me == 0 ? mine : other, me == 0 ? other : mine};
     for (int b = b0; b < b1; ++b) {
-        int x[2];
-        need(b, x);
-        before[b] = at[me];
-        const bool ok = (x[0] == 0 || at[0] + x[0] <= have[0]) && (x[1] == 0 || at[1] + x[1] <= have[1]);
-        int64_t len;
-        const int64_t n = grow(b, len);
-        granted[b] = ok && n > 0;
-        const int64_t asked = n_new != nullptr ? n_new[b] : (len > 0 ? n_all : 0);
-        if (me == 0 && (!ok || (n == 0 && asked != 0))) report(kStatusCapacity);
-        at[0] += x[0];
-        at[1] += x[1];
+        const Grow r = row_of(b);
+        const bool ok = (r.n_core == 0 || at[0] + r.n_core <= have[0]) &&
+                        (r.n_raw == 0 || at[1] + r.n_raw <= have[1]);
+        // (no page is taken for what lies beyond the last free one)
+        before[b] = static_cast<int>(min(at[me], static_cast<int64_t>(INT32_MAX)));
+        column[b] = ok && r.n > 0 ? (me == 0 ? r.core : r.raw) : -1;
+        if (me == 0 && (!ok || r.refused)) report(kStatusCapacity);
+        at[0] += r.n_core;
+        at[1] += r.n_raw;
     }
-    if (threadIdx.x == 0) before[v.B] = total[me];
-    cluster.sync();  // both have read lens and each other's count
-    const Pool &pool = v.pool[me];
-    take_free(pool.ref, pool.pages, total[me], [&](int k, int page) {
+    __syncthreads();
+    auto use = [&](int k, int page) {
         int lo = 0, hi = v.B - 1;  // the row of the k-th wanted page
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -159,25 +182,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScanThreads)
             else
                 hi = mid - 1;
         }
-        if (!granted[lo]) return;
-        int64_t len;
-        const int64_t n = grow(lo, len);
-        const PagedCols a = paged_cols(len, v.g, v.w, v.shift, core);
-        const PagedCols z = paged_cols(len + n, v.g, v.w, v.shift, core);
-        const int col = (me == 0 ? a.core_hi : max(a.raw_hi, z.raw_lo)) + (k - before[lo]);
-        pool.table[static_cast<int64_t>(lo) * pool.cols + col] = page;
+        if (column[lo] < 0) return;
+        pool.table[static_cast<int64_t>(lo) * pool.cols + column[lo] + (k - before[lo])] = page;
         pool.ref[page] = 1;
-    });
+    };
+    const int wanted = static_cast<int>(min(want[me], static_cast<int64_t>(mine)));
+    use_free(bits, 0, free_at[0], wanted, use);
+    int base = free_all[0];
+    for (int chunk = kChunk; chunk < pool.pages && base < wanted; chunk += kChunk) {
+        const int more = free_bits(pool.ref, pool.pages, chunk);
+        int x[1] = {__popc(more)}, n[1];
+        block_scan(x, n, chunk_room[chunk / kChunk & 1]);
+        use_free(more, chunk, base + x[0], wanted, use);
+        base += n[0];
+    }
     __syncthreads();
     // raw pages before the new window go
     if (me == 1)
         for (int b = b0; b < b1; ++b) {
-            if (!granted[b]) continue;
-            int64_t len;
-            const int64_t n = grow(b, len);
-            const PagedCols a = paged_cols(len, v.g, v.w, v.shift, core);
-            const PagedCols z = paged_cols(len + n, v.g, v.w, v.shift, core);
-            for (int col = a.raw_lo; col < min(a.raw_hi, z.raw_lo); ++col) {
+            if (column[b] < 0) continue;
+            const Grow r = row_of(b);
+            for (int col = r.gone; col < r.gone_end; ++col) {
                 int *e = pool.table + static_cast<int64_t>(b) * pool.cols + col;
                 if (*e >= 0 && *e < pool.pages)
                     atomicSub(pool.ref + *e, 1);
@@ -189,14 +214,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kScanThreads)
     cluster.sync();  // lens is read by both until here
     if (me == 0)
         for (int b = b0; b < b1; ++b)
-            if (granted[b]) {
-                int64_t len;
-                const int64_t n = grow(b, len);
-                v.lens[b] = len + n;
+            if (column[b] >= 0) {
+                const Grow r = row_of(b);
+                v.lens[b] = r.len + r.n;
             }
 }
 
-// cca_paged_fill: one warp per packed row (raw) or core row, all heads.
+// cca_paged_fill: a warp takes 32 packed rows (or core rows) of one head:
+// first each lane finds the place of its row, then all copy the rows' keys
+// and values, 8 rows asked for at once (D = 64: 16).
 template <int D>
 __global__ void __launch_bounds__(256)
     fill_kernel(PagedView c, PackedRows K, PackedRows V, const uint16_t *__restrict__ Kc,
@@ -204,6 +230,7 @@ __global__ void __launch_bounds__(256)
                 const int *__restrict__ rows, int S, int64_t total, int64_t m)
 {
     extern __shared__ int scu[];  // [S + 1] offsets, [B] the last sequence that names a row
+    chain_begin();
     int *last = scu + S + 1;
     if (!load_offsets(cu, S, total, scu)) {
         if (blockIdx.x == 0 && threadIdx.x == 0) report(kStatusSeqlens);
@@ -212,56 +239,75 @@ __global__ void __launch_bounds__(256)
     for (int b = threadIdx.x; b < c.B; b += blockDim.x) last[b] = -1;
     __syncthreads();
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
-        const int b = rows[s];
+        const int b = __ldg(rows + s);
         if (b >= 0 && b < c.B) atomicMax(last + b, s);
     }
     __syncthreads();
     if (blockIdx.x == 0)
         for (int s = threadIdx.x; s < S; s += blockDim.x) {
-            const int b = rows[s];
+            const int b = __ldg(rows + s);
             if (b < 0 || b >= c.B || last[b] != s || c.lens[b] != scu[s + 1] - scu[s])
                 report(kStatusPage);
         }
     const int lane = threadIdx.x & 31;
     const int mask = (1 << c.shift) - 1;
-    constexpr int C = D / 8;  // 16-byte chunks of a row
-    const int64_t n = total + (Kc != nullptr ? m : 0);
-    for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; i < n;
-         i += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
-        const bool core = i >= total;
-        const int64_t row = core ? i - total : i;
-        const int s = core ? core_row_sequence(scu, S, c.g, static_cast<int>(row))
-                           : row_sequence(scu, S, row);
-        const int len = scu[s + 1] - scu[s];
-        const int64_t pos = row - (core ? scu[s] / c.g : scu[s]);
-        if (pos < 0 || pos >= (core ? len / c.g : len)) continue;
-        if (!core && pos < window_start(len - 1, c.g, c.w)) continue;
-        const int b = rows[s];
-        if (b < 0 || b >= c.B || last[b] != s || c.lens[b] != len) continue;
-        const int page = core ? own_page_at(c.core_table, c.core_ref, b, c.core_cols,
-                                            pos >> c.shift, c.core_pages)
-                              : own_page_at(c.raw_table, c.raw_ref, b, c.raw_cols, pos >> c.shift,
-                                            c.raw_pages);
-        if (page < 0) {
-            if (lane == 0) report(kStatusPage);
-            continue;
-        }
-        const int slot = static_cast<int>(pos) & mask;
-        for (int x = lane; x < c.Hkv * C; x += 32) {
-            const int h = x / C, e = (x - h * C) * 8;
-            const int64_t to = page_row<D>(page, h, c.Hkv, c.shift, slot) + e;
-            const uint16_t *k, *v;
-            if (core) {
-                k = Kc + (h * m + row) * D + e;
-                v = Vc + (h * m + row) * D + e;
-            } else {
-                k = static_cast<const uint16_t *>(K.data) + h * K.head + row * K.row + e;
-                v = static_cast<const uint16_t *>(V.data) + h * V.head + row * V.row + e;
+    constexpr int CH = D / 8;        // 16-byte chunks of a row
+    constexpr int AT = 32 / (2 * CH);  // rows (keys and values) that the warp copies at once
+    const int e = lane % CH * 8, is_v = lane / CH % 2, sub = lane / (2 * CH);
+    const int64_t raw_units = (total + 31) / 32, core_units = Kc != nullptr ? (m + 31) / 32 : 0;
+    for (int64_t x = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+         x < (raw_units + core_units) * c.Hkv;
+         x += (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5) {
+        const int64_t unit = x / c.Hkv;
+        const int h = static_cast<int>(x - unit * c.Hkv);
+        const bool core = unit >= raw_units;
+        const int64_t row0 = (core ? unit - raw_units : unit) * 32, row = row0 + lane;
+        // this lane's row: its place in the pool, -1 if it has none
+        int64_t to = -1;
+        if (row < (core ? m : total)) {
+            const int s = core ? core_row_sequence(scu, S, c.g, static_cast<int>(row))
+                               : row_sequence(scu, S, row);
+            const int len = scu[s + 1] - scu[s];
+            const int64_t pos = row - (core ? scu[s] / c.g : scu[s]);
+            const int b = __ldg(rows + s);
+            if (pos >= (core ? 0 : window_start(len - 1, c.g, c.w)) && pos >= 0 &&
+                pos < (core ? len / c.g : len) && b >= 0 && b < c.B && last[b] == s &&
+                __ldg(c.lens + b) == len) {
+                const int page = core ? own_page_at(c.core_table, c.core_ref, b, c.core_cols,
+                                                    pos >> c.shift, c.core_pages)
+                                      : own_page_at(c.raw_table, c.raw_ref, b, c.raw_cols,
+                                                    pos >> c.shift, c.raw_pages);
+                if (page >= 0)
+                    to = page_row<D>(page, h, c.Hkv, c.shift, static_cast<int>(pos) & mask);
+                else
+                    report(kStatusPage);
             }
-            *reinterpret_cast<uint4 *>((core ? c.k_core : c.k_raw) + to) =
-                *reinterpret_cast<const uint4 *>(k);
-            *reinterpret_cast<uint4 *>((core ? c.v_core : c.v_raw) + to) =
-                *reinterpret_cast<const uint4 *>(v);
+        }
+        const uint16_t *from;
+        int64_t stride;
+        if (core) {
+            from = (is_v ? Vc : Kc) + (static_cast<int64_t>(h) * m + row0) * D + e;
+            stride = D;
+        } else {
+            const PackedRows &src = is_v ? V : K;
+            from = static_cast<const uint16_t *>(src.data) + h * src.head + row0 * src.row + e;
+            stride = src.row;
+        }
+        uint16_t *pool = (core ? (is_v ? c.v_core : c.k_core) : (is_v ? c.v_raw : c.k_raw)) + e;
+        if (__ballot_sync(0xffffffffu, to >= 0) == 0) continue;
+#pragma unroll 1
+        for (int r0 = 0; r0 < 32; r0 += 8 * AT) {
+            uint4 y[8];
+            int64_t at[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int i = r0 + u * AT + sub;
+                at[u] = __shfl_sync(0xffffffffu, to, i);
+                if (at[u] >= 0) y[u] = ldg_stream(from + i * stride);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (at[u] >= 0) *reinterpret_cast<uint4 *>(pool + at[u]) = y[u];
         }
     }
 }
@@ -302,6 +348,7 @@ __device__ __forceinline__ void used_cols(const TablesView &v, int i, int64_t le
 
 __global__ void __launch_bounds__(256) fork_rows_kernel(ForkView f)
 {
+    chain_begin();
     const TablesView &v = f.v;
     const int b = blockIdx.x;
     const int p = parent_of(f, b);
@@ -354,47 +401,55 @@ __global__ void __launch_bounds__(256) fork_rows_kernel(ForkView f)
 }
 
 // Fork, step 2, a block per pool: free pages for the copies.
-__global__ void __launch_bounds__(kScanThreads) fork_pages_kernel(ForkView f)
+__global__ void __launch_bounds__(kThreads) fork_pages_kernel(ForkView f)
 {
     extern __shared__ int order[];  // [copies] rows that want a page, in order
+    __shared__ int room[kThreads / 32][2], chunk_room[2][kThreads / 32][1];
+    chain_begin();
     const TablesView &v = f.v;
     const int i = blockIdx.x;
     const Pool &pool = v.pool[i];
-    int want = 0;
-    for (int b0 = 0; b0 < v.B; b0 += kScanThreads) {
-        const int b = b0 + threadIdx.x;
-        const bool mine = b < v.B && (f.flags[b] >> i & 1);
-        int total;
-        const int k = want + block_scan(mine ? 1 : 0, total);
-        if (mine) order[k] = b;
-        want += total;
-    }
-    __syncthreads();
-    for (int k = threadIdx.x; k < want; k += kScanThreads) f.list[i][k] = make_int2(-1, -1);
+    const int per = (v.B + kThreads - 1) / kThreads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, v.B), b1 = min(b0 + per, v.B);
+    const int bits = free_bits(pool.ref, pool.pages, 0);
+    int at[2] = {0, __popc(bits)}, all[2];  // wanted, free in the first chunk
+    for (int b = b0; b < b1; ++b) at[0] += f.flags[b] >> i & 1;
+    block_scan(at, all, room);
+    for (int b = b0, k = at[0]; b < b1; ++b)
+        if (f.flags[b] >> i & 1) order[k++] = b;
+    const int want = all[0];
     if (threadIdx.x == 0) f.counts[i] = want;
     __syncthreads();
-    take_free(pool.ref, pool.pages, want, [&](int k, int page) {
-        const int b = order[k];
+    // the entry of a row's open page
+    auto entry = [&](int b) {
         int lo, hi;
         bool open;
-        used_cols(v, i, f.v.lens[parent_of(f, b)], lo, hi, open);
-        int *e = f.tmp[i] + static_cast<int64_t>(b) * pool.cols + hi - 1;
-        if (*e >= 0) f.list[i][k] = make_int2(*e, page);
+        used_cols(v, i, v.lens[parent_of(f, b)], lo, hi, open);
+        return f.tmp[i] + static_cast<int64_t>(b) * pool.cols + hi - 1;
+    };
+    auto use = [&](int k, int page) {
+        int *e = entry(order[k]);
+        f.list[i][k] = make_int2(*e, *e >= 0 ? page : -1);
         *e = page;
         pool.ref[page] = 1;
-    });
+    };
+    use_free(bits, 0, at[1], want, use);
+    int base = all[1];
+    for (int chunk = kChunk; chunk < pool.pages && base < want; chunk += kChunk) {
+        const int more = free_bits(pool.ref, pool.pages, chunk);
+        int x[1] = {__popc(more)}, n[1];
+        block_scan(x, n, chunk_room[chunk / kChunk & 1]);
+        use_free(more, chunk, base + x[0], want, use);
+        base += n[0];
+    }
     // rows that got none
-    __syncthreads();
-    for (int k = threadIdx.x; k < want; k += kScanThreads)
-        if (f.list[i][k].y < 0) {
-            const int b = order[k];
-            int lo, hi;
-            bool open;
-            used_cols(v, i, f.v.lens[parent_of(f, b)], lo, hi, open);
-            f.tmp[i][static_cast<int64_t>(b) * pool.cols + hi - 1] = -1;
-            atomicOr(f.flags + b, 8);
-            report(kStatusCapacity);
-        }
+    for (int k = base + threadIdx.x; k < want; k += kThreads) {
+        const int b = order[k];
+        f.list[i][k] = make_int2(-1, -1);
+        *entry(b) = -1;
+        atomicOr(f.flags + b, 8);
+        report(kStatusCapacity);
+    }
 }
 
 // Copy whole pages of one pool, all layers: list of (from, to).
@@ -432,6 +487,7 @@ __device__ __forceinline__ void copy_pages(const int2 *list, int n, int layers, 
 __global__ void __launch_bounds__(256)
     fork_apply_kernel(ForkView f, PoolData core, PoolData raw, int layers)
 {
+    chain_begin();
     const TablesView &v = f.v;
     for (int b = blockIdx.x; b < v.B; b += gridDim.x) {
         const int flags = f.flags[b];
@@ -465,30 +521,52 @@ __global__ void __launch_bounds__(256)
 }
 
 // Compact, step 1, a block per pool: the k-th page in use at or above the
-// number of pages in use moves to the k-th free page below it.
-__global__ void __launch_bounds__(kScanThreads)
+// number of pages in use moves to the k-th free page below it.  (Before page
+// p lie p - f pages in use, f the free ones before it.)
+__global__ void __launch_bounds__(kThreads)
     compact_plan_kernel(TablesView v, int2 *list0, int2 *list1, int *remap0, int *remap1,
                         int *counts, long long *live_out)
 {
+    __shared__ int room[kThreads / 32][2], chunk_room[2][kThreads / 32][1], moved_s;
+    chain_begin();
     const int i = blockIdx.x;
     const Pool &pool = v.pool[i];
     int2 *list = i == 0 ? list0 : list1;
     int *remap = i == 0 ? remap0 : remap1;
-    const int live = pool.pages - count_free(pool.ref, pool.pages);
-    int moved = 0;
-    for (int p0 = live; p0 < pool.pages; p0 += kScanThreads) {
-        const int p = p0 + threadIdx.x;
-        const bool mine = p < pool.pages && pool.ref[p] != 0;
-        int total;
-        const int k = moved + block_scan(mine ? 1 : 0, total);
-        if (mine) list[k].x = p;
-        moved += total;
+    int bits = free_bits(pool.ref, pool.pages, 0);
+    int at[2] = {__popc(bits), 0}, all[2];  // free in the first chunk, behind it
+    for (int chunk = kChunk; chunk < pool.pages; chunk += kChunk)
+        at[1] += __popc(free_bits(pool.ref, pool.pages, chunk));
+    if (threadIdx.x == 0) moved_s = 0;  // free pages before `live`: pages that move
+    block_scan(at, all, room);
+    const int live = pool.pages - all[0] - all[1];
+    int k = at[0], base = all[0];
+    for (int chunk = 0; chunk < pool.pages; chunk += kChunk) {
+        if (chunk > 0) {
+            bits = free_bits(pool.ref, pool.pages, chunk);
+            int x[1] = {__popc(bits)}, n[1];
+            block_scan(x, n, chunk_room[chunk / kChunk & 1]);
+            k = base + x[0];
+            base += n[0];
+        }
+        const int p0 = chunk + threadIdx.x * 4;
+        if (live < pool.pages && live >= p0 && live < p0 + 4)
+            moved_s = k + __popc(bits & ((1 << (live - p0)) - 1));
+        __syncthreads();
+        for (int u = 0; u < 4 && p0 + u < pool.pages; ++u) {
+            const int p = p0 + u;
+            if (bits >> u & 1) {
+                if (p < live) list[k].y = p;
+                ++k;
+            } else if (p >= live) {
+                list[p - k - (live - moved_s)].x = p;
+            }
+        }
     }
     __syncthreads();
-    take_free(pool.ref, live, moved, [&](int k, int page) { list[k].y = page; });
-    __syncthreads();
-    for (int k = threadIdx.x; k < moved; k += kScanThreads) {
-        const int2 ft = list[k];
+    const int moved = moved_s;
+    for (int j = threadIdx.x; j < moved; j += kThreads) {
+        const int2 ft = list[j];
         remap[ft.x] = ft.y;
         pool.ref[ft.y] = pool.ref[ft.x];
         pool.ref[ft.x] = 0;
@@ -506,6 +584,7 @@ __global__ void __launch_bounds__(256)
                          const int *remap1, const int *counts, PoolData core, PoolData raw,
                          int layers)
 {
+    chain_begin();
     for (int b = blockIdx.x; b < v.B; b += gridDim.x)
         for (int i = 0; i < 2; ++i) {
             const Pool &pool = v.pool[i];
@@ -586,9 +665,8 @@ PagedWorkspace paged_workspace(const cca_paged_cache &c)
 cudaError_t launch_paged_reserve(const cca_paged_cache &c, const long long *n_new, long long n,
                                  cudaStream_t s)
 {
-    const size_t smem = sizeof(int) * (2 * c.B + 1);
-    reserve_kernel<<<2, kScanThreads, smem, s>>>(tables_view(c), n_new, n);
-    return cudaGetLastError();
+    return launch_chained(reserve_kernel, 2, kThreads, sizeof(int) * 2 * c.B, s, tables_view(c),
+                          n_new, n);
 }
 
 cudaError_t launch_paged_fill(const cca_paged_cache &c, int layer, const PackedRows &K,
@@ -597,7 +675,8 @@ cudaError_t launch_paged_fill(const cca_paged_cache &c, int layer, const PackedR
 {
     const PagedView v = paged_view(c, layer);
     if (c.core_cols == 0) Kc = Vc = nullptr;
-    const int64_t m = total / c.g, warps = total + m;
+    const int64_t m = total / c.g;
+    const int64_t warps = ((total + 31) / 32 + (Kc != nullptr ? (m + 31) / 32 : 0)) * c.Hkv;
     const int64_t want = (warps + 7) / 8;
     const int most = copy_grid();
     const int grid = static_cast<int>(want < most ? want : most);
@@ -608,9 +687,8 @@ cudaError_t launch_paged_fill(const cca_paged_cache &c, int layer, const PackedR
             e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      static_cast<int>(smem));
         if (e != cudaSuccess) return;
-        kern<<<grid, 256, smem, s>>>(v, K, V, static_cast<const uint16_t *>(Kc),
-                                     static_cast<const uint16_t *>(Vc), cu, rows, S, total, m);
-        e = cudaGetLastError();
+        e = launch_chained(kern, grid, 256, smem, s, v, K, V, static_cast<const uint16_t *>(Kc),
+                           static_cast<const uint16_t *>(Vc), cu, rows, S, total, m);
     };
     if (c.d == 128)
         go(fill_kernel<128>);
@@ -634,11 +712,13 @@ cudaError_t launch_paged_fork(const cca_paged_cache &c, const int *parent, void 
     f.list[0] = reinterpret_cast<int2 *>(base + w.lists);
     f.list[1] = f.list[0] + c.B;
     f.counts = reinterpret_cast<int *>(base + w.counts);
-    fork_rows_kernel<<<c.B, 256, 0, s>>>(f);
-    fork_pages_kernel<<<2, kScanThreads, sizeof(int) * c.B, s>>>(f);
-    fork_apply_kernel<<<copy_grid(), 256, 0, s>>>(f, pool_data(c, true), pool_data(c, false),
-                                                  c.layers);
-    return cudaGetLastError();
+    cudaError_t e = launch_chained(fork_rows_kernel, c.B, 256, 0, s, f);
+    if (e == cudaSuccess)
+        e = launch_chained(fork_pages_kernel, 2, kThreads, sizeof(int) * c.B, s, f);
+    if (e == cudaSuccess)
+        e = launch_chained(fork_apply_kernel, copy_grid(), 256, 0, s, f, pool_data(c, true),
+                           pool_data(c, false), c.layers);
+    return e;
 }
 
 cudaError_t launch_paged_compact(const cca_paged_cache &c, long long *live, void *workspace,
@@ -650,11 +730,11 @@ cudaError_t launch_paged_compact(const cca_paged_cache &c, long long *live, void
     int2 *list0 = reinterpret_cast<int2 *>(base + w.lists), *list1 = list0 + c.core_pages;
     int *remap0 = reinterpret_cast<int *>(list1 + c.raw_pages), *remap1 = remap0 + c.core_pages;
     int *counts = reinterpret_cast<int *>(base + w.counts);
-    compact_plan_kernel<<<2, kScanThreads, 0, s>>>(v, list0, list1, remap0, remap1, counts, live);
-    compact_apply_kernel<<<copy_grid(), 256, 0, s>>>(v, list0, list1, remap0, remap1, counts,
-                                                     pool_data(c, true), pool_data(c, false),
-                                                     c.layers);
-    return cudaGetLastError();
+    const cudaError_t e = launch_chained(compact_plan_kernel, 2, kThreads, 0, s, v, list0, list1,
+                                         remap0, remap1, counts, live);
+    if (e != cudaSuccess) return e;
+    return launch_chained(compact_apply_kernel, copy_grid(), 256, 0, s, v, list0, list1, remap0,
+                          remap1, counts, pool_data(c, true), pool_data(c, false), c.layers);
 }
 
 cudaError_t paged_tables_status_read_clear(unsigned int *v)

@@ -155,12 +155,12 @@ __device__ __forceinline__ bool pool_group_warp(KeyRow key_row, ValRow val_row,
 // The warp is cut into RPW = 32 / (D/8) row slots of D/8 lanes; lane l owns
 // dims [8*(l % (D/8)), +8) of rows i with i % RPW == l / (D/8), loaded as
 // 16-byte vectors.  All of the group's key rows are requested before any
-// arithmetic (then all its value rows, for G = 32 only once the keys are
-// pooled), so each warp keeps G * 2 * D bytes in flight.  Scores are reduced
+// arithmetic (then all its value rows; without EARLY_V, as for G = 32, only
+// once the keys are pooled), so each warp keeps G * 2 * D bytes in flight.  Scores are reduced
 // over the lanes of a row; the pooled sums are reduced over the row slots.
 // Same arithmetic as pool_group_warp: fp32 scores, fp32 softmax per query
 // head, mean over heads, fp32 weighted sums, fp16 stores.
-template <int D, int G, class KeyRow, class ValRow, class QRow>
+template <int D, int G, bool EARLY_V = (G <= 16), class KeyRow, class ValRow, class QRow>
 __device__ __forceinline__ bool pool_group_warp_fast(KeyRow key_row, ValRow val_row,
                                                      QRow q_row, int r,
                                                      float scale_log2, float *scratch,
@@ -182,7 +182,7 @@ __device__ __forceinline__ bool pool_group_warp_fast(KeyRow key_row, ValRow val_
 #pragma unroll
     for (int n = 0; n < NR; ++n)
         kv[n] = *reinterpret_cast<const uint4 *>(key_row(n * RPW + slot) + kl * 8);
-    if (G <= 16) {
+    if (EARLY_V) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
             vv[n] = *reinterpret_cast<const uint4 *>(val_row(n * RPW + slot) + kl * 8);
@@ -236,7 +236,7 @@ __device__ __forceinline__ bool pool_group_warp_fast(KeyRow key_row, ValRow val_
 #pragma unroll
         for (int e = 0; e < 8; ++e) ak[e] = fmaf(a, kf[e], ak[e]);
     }
-    if (G > 16) {
+    if (!EARLY_V) {
 #pragma unroll
         for (int n = 0; n < NR; ++n)
             vv[n] = *reinterpret_cast<const uint4 *>(val_row(n * RPW + slot) + kl * 8);

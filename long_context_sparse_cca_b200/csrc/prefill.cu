@@ -49,6 +49,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "packed.cuh"
 #include "sm100.cuh"
 
 namespace cca {
@@ -59,6 +60,11 @@ namespace {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
 constexpr float kRescaleThreshold = 15.0f;  // log2 units: P stays <= 2^15 (fp16 range)
+
+// Packed sequences: up to so many sequences and query blocks every CTA
+// orders the blocks by itself, beyond that a kernel of its own does.  (The
+// kernel takes 3 us; 64 sequences and 256 blocks fit beside D = 128's tiles.)
+constexpr int kInlineSeqs = 64, kInlineBlocks = 256;
 
 template <int D>
 struct Pf {
@@ -72,6 +78,7 @@ struct Pf {
     static constexpr int OFF_V = OFF_K + KST * TILE_BYTES;
     static constexpr int OFF_BAR = OFF_V + VST * TILE_BYTES;
     static constexpr int SMEM = OFF_BAR + 512 + 1024;  // + barriers + align slack
+    static constexpr int SMEM_PK = SMEM + kInlineBlocks * 4 + (kInlineSeqs + 1) * 4;
     static constexpr uint32_t S_COL = 0;          // S, shared by the halves
     static constexpr uint32_t P_COL = 128;        // P of half h at 128 + h * 64
     static constexpr uint32_t O_COL = 256;        // O of half h at 256 + h * D
@@ -90,7 +97,10 @@ struct Params {
     // packed sequences (PK instance): the query blocks in the order in which
     // they are taken, and the output's strides
     const int4 *blocks;     // {first row, rows, block, first core row} of its sequence
-    const int *block_count;
+    const int *block_count; // or, where both are null, each CTA orders them itself:
+    const int *cu;
+    int S;
+    int64_t total;
     int64_t o_row, o_head;
 };
 
@@ -103,11 +113,20 @@ __device__ __forceinline__ int ws_of(int t, int g, int w)
 // Geometry of one 256-row block.
 struct Geom {
     int row0, core0;           // PK: first row and first core row of the sequence
-    int T;                     // rows of the sequence
+    int T, m;                  // rows and core rows of the sequence
     int b, hq, h, t0, tlast;
     int ws_lo;                 // ws(t0): first local key
     int n_local, n_core_tiles, n_tiles;
 };
+
+__device__ __forceinline__ bool tile_is_core(const Geom &G, int j);
+__device__ __forceinline__ int tile_key0(const Geom &G, int j);
+
+// Rows of tile j behind the end of the sequence.
+__device__ __forceinline__ int rows_behind(const Geom &G, int j)
+{
+    return tile_key0(G, j) + 128 - (tile_is_core(G, j) ? G.m : G.T);
+}
 
 __device__ __forceinline__ void geom_tiles(Geom &G, int blk, const Params &p)
 {
@@ -122,8 +141,10 @@ __device__ __forceinline__ void geom_tiles(Geom &G, int blk, const Params &p)
 
 // HM: head-major item order (all blocks of a head before the next head).
 // PK: the blocks of packed sequences, from the list (most key tiles first).
+// scu, list: the offsets and the blocks' order, if this CTA has made it.
 template <bool HM, bool PK>
-__device__ __forceinline__ Geom geom(int item, int n_blocks, const Params &p)
+__device__ __forceinline__ Geom geom(int item, int n_blocks, const Params &p, const int *scu,
+                                     const int *list)
 {
     Geom G;
     if constexpr (PK) {
@@ -132,20 +153,39 @@ __device__ __forceinline__ Geom geom(int item, int n_blocks, const Params &p)
             G.hq = item / n_blocks;
             i = item - G.hq * n_blocks;
         } else {
+            // every other round of the CTAs goes backwards: who took the
+            // longest block of one round takes the shortest of the next
+            // (3840 tiles in blocks of 1 to 16 over 148 CTAs: at most 33 a
+            // CTA instead of 39)
+            const int n = gridDim.x, round = item / n;
+            if ((round & 1) && (round + 1) * n <= n_blocks * p.Hq)
+                item = (2 * round + 1) * n - 1 - item;
             i = item / p.Hq;
             G.hq = item - i * p.Hq;
         }
-        const int4 e = __ldg(p.blocks + i);
-        G.row0 = e.x;
-        G.T = e.y;
-        G.core0 = e.w;
+        int blk;
+        if (p.blocks == nullptr) {
+            const int s = list[i] & 255;
+            blk = list[i] >> 8;
+            G.row0 = scu[s];
+            G.T = scu[s + 1] - G.row0;
+            G.core0 = G.row0 / p.g;
+        } else {
+            const int4 e = __ldg(p.blocks + i);
+            G.row0 = e.x;
+            G.T = e.y;
+            blk = e.z;
+            G.core0 = e.w;
+        }
+        G.m = G.T / p.g;
         G.b = 0;
         G.h = G.hq / p.r;
-        geom_tiles(G, e.z, p);
+        geom_tiles(G, blk, p);
         return G;
     }
     G.row0 = G.core0 = 0;
     G.T = p.T;
+    G.m = p.m;
     const int bhq_count = p.B * p.Hq;
     // Latest blocks (most core tiles) first.  Across heads when the core
     // rows of all heads fit in L2, so that concurrent items have equal
@@ -326,11 +366,28 @@ __global__ void __launch_bounds__(352, 1)
             tma_prefetch_desc(&tmVc);
         }
     }
+    int *scu = nullptr, *list = nullptr;
+    int n_blocks = p.n_blocks;
+    if constexpr (PK) {
+        chain_begin();
+        if (p.blocks != nullptr) {
+            n_blocks = __ldg(p.block_count);
+        } else {
+            list = reinterpret_cast<int *>(smem + C::OFF_BAR + 512);
+            scu = list + kInlineBlocks;
+            const bool good = load_offsets(p.cu, p.S, p.total, scu);
+            PackedPair pair = {0, -1};
+            if (good && threadIdx.x < p.total / 256 + p.S) pair = packed_pair(scu, p.S, threadIdx.x);
+            if (pair.blk >= 0) list[packed_place(scu, p.S, pair)] = pair.s | pair.blk << 8;
+            n_blocks = __syncthreads_count(pair.blk >= 0);
+            if (!good && blockIdx.x == 0 && threadIdx.x == 0)
+                atomicOr(&g_prefill_status, kStatusSeqlens);
+        }
+    }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = bars->tmem_base;
-    const int n_blocks = PK ? __ldg(p.block_count) : p.n_blocks;
     const int n_items = PK ? n_blocks * p.Hq : p.n_items;
 
     if (warp == 8) {
@@ -339,7 +396,7 @@ __global__ void __launch_bounds__(352, 1)
             uint32_t kc = 0, vc = 0, qc = 0;
             bool ok = true;
             for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
-                const Geom G = geom<HM, PK>(item, n_blocks, p);
+                const Geom G = geom<HM, PK>(item, n_blocks, p, scu, list);
                 if (qc > 0 && !(ok = lane_wait(&bars->q_empty, (qc - 1) & 1, bars))) break;
                 mbar_arrive_expect_tx(&bars->q_full, 2 * C::TILE_BYTES);
                 for (int hh = 0; hh < 2; ++hh)
@@ -426,7 +483,7 @@ __global__ void __launch_bounds__(352, 1)
                 };
                 for (int item = blockIdx.x; ok && item < n_items;
                      item += gridDim.x, ++k) {
-                    const Geom G = geom<HM, PK>(item, n_blocks, p);
+                    const Geom G = geom<HM, PK>(item, n_blocks, p, scu, list);
                     if (!(ok = lane_wait(&bars->q_full, k & 1, bars))) break;
                     for (int j = 0; ok && j < G.n_tiles; ++j, ++it) {
                         const bool core = tile_is_core(G, j);
@@ -472,7 +529,7 @@ __global__ void __launch_bounds__(352, 1)
                 };
                 for (int item = blockIdx.x; ok && item < n_items;
                      item += gridDim.x, ++k) {
-                    const Geom G = geom<HM, PK>(item, n_blocks, p);
+                    const Geom G = geom<HM, PK>(item, n_blocks, p, scu, list);
                     for (int j = 0; ok && j < G.n_tiles; ++j, ++it) {
                         const bool core = tile_is_core(G, j);
                         const uint32_t sv = vc % C::VST;
@@ -509,7 +566,7 @@ __global__ void __launch_bounds__(352, 1)
         uint32_t it = 0;  // key tiles over all items
         bool ok = true;
         for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
-            const Geom G = geom<HM, PK>(item, n_blocks, p);
+            const Geom G = geom<HM, PK>(item, n_blocks, p, scu, list);
             const bool core_block = G.n_core_tiles > 0;
             const int t0h = G.t0 + hh * 128;       // first row of this half
             const int t = t0h + row;
@@ -544,6 +601,23 @@ __global__ void __launch_bounds__(352, 1)
                     for (int e = 0; e < 128; ++e) {
                         const int key = key0 + e;
                         if (key < lo || key > hi) x[e] = -INFINITY;
+                    }
+                    if (PK && hh == 0 && rows_behind(G, j) > 0) {
+                        // half A's P V is issued first and waits for these
+                        // warps; tiles like this one are masked in every
+                        // half that has rows, so no other tile gets here
+                        // (beside P, in every tile's path, the same code
+                        // cost 4% at 32K)
+                        const uint32_t sv = it % C::VST;
+                        if (!(ok = warp_wait(&bars->v_full[sv], (it / C::VST) & 1, bars))) break;
+                        if (row >= 128 - rows_behind(G, j)) {
+#pragma unroll 1
+                            for (int c = 0; c < C::NBOX * 8; ++c)
+                                *reinterpret_cast<uint4 *>(sV + sv * C::TILE_BYTES +
+                                                           (c >> 3) * C::BOX_BYTES + row * 128 +
+                                                           (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            fence_proxy_async_smem();
+                        }
                     }
                 }
                 const float m_tile = row_max128(x) * p.scale_log2;
@@ -599,23 +673,6 @@ __global__ void __launch_bounds__(352, 1)
                     }
                 }
                 tmem_wait_st();
-                if (PK && hh == 0) {
-                    // value rows behind the sequence's end (see above): half
-                    // A's P V is issued first and waits for these warps
-                    const int last = core ? G.T / p.g - 1 : G.T - 1;
-                    if (key0 + 127 > last) {
-                        const uint32_t sv = it % C::VST;
-                        if (!(ok = warp_wait(&bars->v_full[sv], (it / C::VST) & 1, bars))) break;
-                        if (key0 + row > last) {
-#pragma unroll
-                            for (int c = 0; c < C::NBOX * 8; ++c)
-                                *reinterpret_cast<uint4 *>(sV + sv * C::TILE_BYTES +
-                                                           (c >> 3) * C::BOX_BYTES + row * 128 +
-                                                           (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            fence_proxy_async_smem();
-                        }
-                    }
-                }
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->p_full[hh]);
@@ -741,7 +798,9 @@ cudaError_t launch_d(const void *Q, const void *K, const void *V, const void *Kc
     p.o_f32 = o_f32 ? 1 : 0;
     p.lse = lse;
     p.blocks = nullptr;
-    p.block_count = nullptr;
+    p.block_count = p.cu = nullptr;
+    p.S = 0;
+    p.total = 0;
     p.o_row = p.o_head = 0;
     int dev = 0, sms = 148, l2 = 0;
     cudaGetDevice(&dev);
@@ -763,8 +822,8 @@ cudaError_t launch_d(const void *Q, const void *K, const void *V, const void *Kc
 template <int D>
 cudaError_t launch_packed_d(const PackedRows &Q, const PackedRows &K, const PackedRows &V,
                             const void *Kc, const void *Vc, const PackedRows &O, bool o_f32,
-                            const int4 *blocks, const int *block_count, int64_t max_blocks, int Hq,
-                            int Hkv, int64_t total, int g, int w, cudaStream_t s)
+                            const int4 *blocks, const int *block_count, const int *cu, int S,
+                            int Hq, int Hkv, int64_t total, int g, int w, cudaStream_t s)
 {
     using C = Pf<D>;
     CUtensorMap mQ, mK, mV, mKc, mVc;
@@ -795,13 +854,16 @@ cudaError_t launch_packed_d(const PackedRows &Q, const PackedRows &K, const Pack
     p.lse = nullptr;
     p.blocks = blocks;
     p.block_count = block_count;
+    p.cu = cu;
+    p.S = S;
+    p.total = total;
     p.o_row = O.row;
     p.o_head = O.head;
     int dev = 0, sms = 148, l2 = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev);
-    const int64_t most = max_blocks * Hq;
+    const int64_t most = packed_max_blocks(S, total) * Hq;
     const int grid = static_cast<int>(most < sms ? most : sms);
     // head by head, as above, when what a query may look far back into (the
     // core rows; for plain causal attention all keys and values) exceeds
@@ -810,9 +872,11 @@ cudaError_t launch_packed_d(const PackedRows &Q, const PackedRows &K, const Pack
     const bool hm = 4.0 * static_cast<double>(Hkv) * far_rows * D > 0.5 * static_cast<double>(l2);
     auto kern = hm ? prefill_kernel<D, false, true, true> : prefill_kernel<D, false, false, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         C::SMEM);
+                                         C::SMEM_PK);
     if (e != cudaSuccess) return e;
-    kern<<<grid, C::THREADS, C::SMEM, s>>>(mQ, mK, mV, mKc, mVc, p);
+    // (not launch_chained: set up while the pooling still ran, the attention
+    // took 8% to 20% longer at 16K to 32K tokens)
+    kern<<<grid, C::THREADS, C::SMEM_PK, s>>>(mQ, mK, mV, mKc, mVc, p);
     return cudaGetLastError();
 }
 
@@ -825,13 +889,17 @@ cudaError_t launch_prefill_packed(const PackedRows &Q, const PackedRows &K, cons
 {
     int *count = static_cast<int *>(workspace);
     int4 *blocks = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + 256);
-    const cudaError_t e = launch_packed_plan(cu, S, total, g, blocks, count, s);
-    if (e != cudaSuccess) return e;
-    const int64_t most = packed_max_blocks(S, total);
+    if (S <= kInlineSeqs && packed_max_blocks(S, total) <= kInlineBlocks) {
+        count = nullptr;
+        blocks = nullptr;
+    } else {
+        const cudaError_t e = launch_packed_plan(cu, S, total, g, blocks, count, s);
+        if (e != cudaSuccess) return e;
+    }
     if (d == 128)
-        return launch_packed_d<128>(Q, K, V, Kc, Vc, O, o_f32, blocks, count, most, Hq, Hkv, total,
+        return launch_packed_d<128>(Q, K, V, Kc, Vc, O, o_f32, blocks, count, cu, S, Hq, Hkv, total,
                                     g, w, s);
-    return launch_packed_d<64>(Q, K, V, Kc, Vc, O, o_f32, blocks, count, most, Hq, Hkv, total, g, w,
+    return launch_packed_d<64>(Q, K, V, Kc, Vc, O, o_f32, blocks, count, cu, S, Hq, Hkv, total, g, w,
                                s);
 }
 

@@ -190,8 +190,7 @@ def test_new_statuses():
 
 
 def test_binding_checks():
-    """Devices, types and shapes, before the library is called (CPU tensors:
-    whatever passes the checks before is refused for its device)."""
+    """Devices, types and shapes, before the library is called."""
     import torch
     q = torch.zeros((4, 300, 64), dtype=torch.bfloat16)
     k = torch.zeros((2, 300, 64), dtype=torch.bfloat16)
@@ -201,15 +200,18 @@ def test_binding_checks():
     with pytest.raises(ValueError, match="CUDA"):
         cca.cca_attn_prefill_packed(q, k, k, None, None, cu, 16, 1 << 30)
     with pytest.raises(ValueError, match="Q must be a torch.bfloat16"):
-        cca.cca_pool_packed(q.float(), k, k, cu, 16)
+        cca._rows(q.float(), "Q", (4, 300, 64), torch.bfloat16, 0)
     with pytest.raises(ValueError, match="rows of Q must be contiguous"):
-        cca.cca_pool_packed(q.transpose(1, 2).contiguous().transpose(1, 2), k, k, cu, 16)
+        cca._rows(q.transpose(1, 2).contiguous().transpose(1, 2), "Q", (4, 300, 64),
+                  torch.bfloat16, 0)
+    with pytest.raises(ValueError, match="device 0"):
+        cca._rows(q, "Q", (4, 300, 64), torch.bfloat16, 0)
     with pytest.raises(ValueError, match="int32"):
-        cca._offsets(cu.long())
+        cca._offsets(cu.long(), 0)
     with pytest.raises(ValueError, match="K must be"):
-        cca._rows(k[:, :299], "K", (2, 300, 64))
+        cca._rows(k[:, :299], "K", (2, 300, 64), torch.bfloat16, 0)
     with pytest.raises(ValueError, match="heads, total, d"):
-        cca.cca_pool_packed(q[None], k, k, cu, 16)
+        cca._packed_shapes(q[None], k)
     with pytest.raises(ValueError):
         cca.PagedCache(0, 4, 2, 64, 16, 64, 16, 8, 16, 200, device="cpu")
     c = cca.PagedCache(3, 4, 2, 64, 16, 64, 16, 8, 16, 200, device="cpu")
@@ -238,7 +240,9 @@ def test_binding_refuses_another_device(monkeypatch):
     import torch
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     with pytest.raises(ValueError, match="not the current device"):
-        cca._here(_Fake(), "Q")
+        cca._device(_Fake(), "Q")
+    with pytest.raises(ValueError, match="device 0"):
+        cca._here(_Fake(), "K", 0)
 
 
 def test_paged_cache_state_round_trip():
@@ -316,6 +320,9 @@ def _packed_items(lens, g, w, Hq, cta, grid):
                      for blk in range(-(-n // 256))))
     out = []
     for item in range(cta, len(blocks) * Hq, grid):
+        k = item // grid
+        if k % 2 and (k + 1) * grid <= len(blocks) * Hq:
+            item = (2 * k + 1) * grid - 1 - item
         _, _, n, blk = blocks[item // Hq]
         t0, tlast = blk * 256, min(blk * 256 + 255, n - 1)
         nl = (tlast - pm.ws_of(t0, g, w) + 128) // 128
@@ -336,10 +343,10 @@ def _first_half_softmax(sim, items, VST=2, wait=True):
             yield from sim.wait("s_full0", it)
             sim.arrive("s_free0")
             yield
-            if it > 0:
-                yield from sim.wait("o_bar0", it - 1)
             if wait and behind[j]:
                 yield from sim.wait(f"v_full{it % VST}", it // VST)
+            if it > 0:
+                yield from sim.wait("o_bar0", it - 1)
             sim.arrive("p_full0")
             if nc > 0 and j == nl - 1:
                 sim.arrive("qh_full0")
