@@ -98,8 +98,14 @@ __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_
     }
 }
 
-// 16 bytes from global to shared memory, or zeros.
-__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool ok)
+// 16 bytes from global to shared memory.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
+// The same, or zeros.
+__device__ __forceinline__ void copy16_or_0(uint32_t to, const void *from, bool ok)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from),
                  "r"(ok ? 16 : 0)
@@ -120,11 +126,16 @@ __device__ __forceinline__ RowTiles row_tiles(const PagedView &c, int b, bool &o
     const int64_t len = __ldg(c.lens + b);
     over = len > c.longest;  // a row longer than its table is taken as free
     r.len = over || len < 0 ? 0 : len;
-    const PagedRow p = paged_row(r.len, c.g, c.w);
-    r.ws = p.ws;
-    r.n_core = p.n_core;
-    r.core = static_cast<int>((p.n_core + KEYS - 1) / KEYS);
-    r.all = r.len == 0 ? 0 : r.core + static_cast<int>(((r.len + KEYS - 1) / KEYS) - p.ws / KEYS);
+    const int64_t past = r.len - 1 - c.w;  // as paged_row, but for the 32-bit division
+    if (past < c.g)
+        r.n_core = 0;
+    else if (past >> 32 == 0)
+        r.n_core = static_cast<uint32_t>(past) / static_cast<uint32_t>(c.g);
+    else
+        r.n_core = past / c.g;
+    r.ws = r.n_core * c.g;
+    r.core = static_cast<int>((r.n_core + KEYS - 1) / KEYS);
+    r.all = r.len == 0 ? 0 : r.core + static_cast<int>(((r.len + KEYS - 1) / KEYS) - r.ws / KEYS);
     return r;
 }
 
@@ -189,7 +200,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     __shared__ int4 meta[kWarps][STAGES];  // row, head and flags of the tiles in the ring
     __shared__ int ids[2 * kWarps];        // pairs of the partial results, -1: none
     __shared__ int pools_s[kWarps];
-    __shared__ int3 join_s[2];  // parts to join (0: not here), CTA of the first, its slot
+    __shared__ unsigned int arrived_s[2];  // CTAs at a shared pair before this one
+    __shared__ int3 join_s[2];             // its parts, CTA of the first, its slot
 
     chain_begin();
     if (tid < 2 * kWarps) ids[tid] = -1;
@@ -237,12 +249,19 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     auto copy_rows = [&](uint32_t to, const uint16_t *from, const uint16_t *in, int tlo, int thi,
                          int fresh) {
         const uint16_t *src = from + from_off;
+        if (tlo == 0 && thi == kPart && fresh < 0) {  // as nearly always
 #pragma unroll
+            for (int u = 0; u < kPart / RPC; ++u)
+                copy16(to + to_off[u % NU] + u / NU * 1024, src + u * RPC * D);
+            return;
+        }
+#pragma unroll 1
         for (int u = 0; u < kPart / RPC; ++u) {
             const int x = u * RPC + lane / CH;
             const bool is_new = STEP && x == fresh;
-            copy16(to + to_off[u % NU] + u / NU * 1024, is_new ? in + cc * 8 : src + u * RPC * D,
-                   is_new || (x >= tlo && x < thi));
+            copy16_or_0(to + (cc >> 3) * (kPart * 128) + x * 128 + (((cc ^ x) & 7) << 4),
+                        is_new ? in + cc * 8 : src + u * RPC * D,
+                        is_new || (x >= tlo && x < thi));
         }
     };
     auto commit = [&]() { asm volatile("cp.async.commit_group;" ::: "memory"); };
@@ -504,8 +523,12 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         static_cast<int>(min(static_cast<int64_t>(gridDim.x), (total + kWarps - 1) / kWarps));
     if (blockIdx.x >= n_ctas) return;
     // the first tile at or behind place x of the list
-    auto tile_from = [&](int64_t x) {
-        if (x >= total) return first_of(c.B);
+    struct Place {
+        int64_t tile;
+        int b, h, i;
+    };
+    auto place_from = [&](int64_t x) {
+        if (x >= total) return Place{first_of(c.B), c.B, 0, 0};
         int a = 0, z = c.B - 1;
         while (a < z) {
             const int mid = (a + z + 1) >> 1;
@@ -514,9 +537,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             else
                 z = mid - 1;
         }
-        const int64_t n = tiles_before(a + 1) - tiles_before(a);
-        const int64_t in_row = x - cost_of(a), h = in_row / (n + kPairTiles);
-        return first_of(a) + h * n + max(static_cast<int64_t>(0), in_row - h * (n + kPairTiles) - kPairTiles);
+        const int n = static_cast<int>(tiles_before(a + 1) - tiles_before(a));
+        const int64_t in_row = x - cost_of(a);
+        const int h = static_cast<int>(in_row >> 32 == 0
+                                           ? static_cast<uint32_t>(in_row) / (n + kPairTiles)
+                                           : in_row / (n + kPairTiles));
+        const int i = static_cast<int>(
+            max(static_cast<int64_t>(0),
+                in_row - static_cast<int64_t>(h) * (n + kPairTiles) - kPairTiles));
+        return Place{first_of(a) + static_cast<int64_t>(h) * n + i, a, h, i};
     };
     // the CTA that has tile i of a head's n in row b
     auto cta_of = [&](int b, int h, int64_t n, int64_t i) {
@@ -524,21 +553,41 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         return static_cast<int>(((x + 1) * n_ctas - 1) / total);
     };
     const int64_t my_lo = total * blockIdx.x / n_ctas, my_hi = total * (blockIdx.x + 1) / n_ctas;
-    const int64_t cta_lo = tile_from(my_lo), cta_hi = tile_from(my_hi);
-    int64_t lo = my_lo, hi = my_lo;
+    int64_t cta_lo, cta_hi;
+    int n_tiles, at_b, at_h, at_i;  // this warp's tiles; the first one's row, head and place
     {
-        int all = 0, upto = 0;
-        for (int w = 0; STEP && w < kWarps; ++w) all += pools_s[w];
-        for (int w = 0; w <= warp; ++w) {
-            if (STEP) upto += pools_s[w];
-            lo = hi;
-            hi = my_lo + (my_hi - my_lo + kPoolTiles * all) * (w + 1) / kWarps - kPoolTiles * upto;
-            hi = w + 1 == kWarps ? my_hi : max(lo, min(my_hi, hi));
+        // lane w: where warp w's part ends
+        const int mine = STEP && lane < kWarps ? pools_s[lane] : 0;
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
         }
-        lo = tile_from(lo);
-        hi = tile_from(hi);
+        const int all = __shfl_sync(0xffffffffu, upto, 31);
+        const int64_t n = my_hi - my_lo;
+        int64_t end = (n + kPoolTiles * all) * (lane + 1) / kWarps - kPoolTiles * upto;
+        end = lane + 1 >= kWarps ? n : max(static_cast<int64_t>(0), min(n, end));
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end = max(end, y);
+        }
+        const int64_t lo = __shfl_sync(0xffffffffu, end, max(warp - 1, 0));
+        const int64_t hi = __shfl_sync(0xffffffffu, end, warp);
+        // lanes 0 and 1: this warp's part, 2 and 3: the CTA's stretch
+        const Place at = place_from(lane == 0   ? my_lo + (warp > 0 ? lo : 0)
+                                    : lane == 1 ? my_lo + hi
+                                    : lane == 2 ? my_lo
+                                                : my_hi);
+        cta_lo = __shfl_sync(0xffffffffu, at.tile, 2);
+        cta_hi = __shfl_sync(0xffffffffu, at.tile, 3);
+        n_tiles = static_cast<int>(__shfl_sync(0xffffffffu, at.tile, 1) -
+                                   __shfl_sync(0xffffffffu, at.tile, 0));
+        at_b = __shfl_sync(0xffffffffu, at.b, 0);
+        at_h = __shfl_sync(0xffffffffu, at.h, 0);
+        at_i = __shfl_sync(0xffffffffu, at.i, 0);
     }
-    const int n_tiles = static_cast<int>(hi - lo);
 
     // The last row whose tiles begin at or before x.
     auto row_at = [&](int64_t x) {
@@ -555,13 +604,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 
     if (n_tiles > 0) {
         bool over, bad = false;
-        int at_b = row_at(lo), at_h, at_i;  // row, head, tile of the pair: the next one to ask for
         RowTiles row = row_tiles<P::KEYS>(c, at_b, over);
-        {
-            const int64_t in_row = lo - first_of(at_b);
-            at_h = static_cast<int>(in_row / row.all);
-            at_i = static_cast<int>(in_row - static_cast<int64_t>(at_h) * row.all);
-        }
         int from = 0, id = 0;  // pages of the parts PARTS * from + lane of the pair
         auto load_ids = [&]() {
             from = at_i;
@@ -657,20 +700,25 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 #pragma unroll
             for (int x = 0; x < QR; ++x) {
                 float top = -INFINITY;
+                if (!all) {
 #pragma unroll
-                for (int n = 0; n < NK; ++n)
+                    for (int n = 0; n < NK; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float &y = s[n][2 * x + e];
-                        y *= q_scale[x];
-                        if (!all) {  // a missing page leaves the newest row alone
+                        for (int e = 0; e < 2; ++e) {
+                            // a missing page leaves the newest row alone
                             const int key = n * 8 + qj * 2 + e;
                             const bool ok = flags & (kPage << (n / 2))
                                                 ? key >= tlo && key < thi
                                                 : (flags & kNewest) && key == thi - 1;
-                            if (!ok) y = -INFINITY;
+                            if (!ok) s[n][2 * x + e] = -INFINITY;
                         }
-                        top = fmaxf(top, y);
+                }
+#pragma unroll
+                for (int n = 0; n < NK; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        s[n][2 * x + e] *= q_scale[x];
+                        top = fmaxf(top, s[n][2 * x + e]);
                     }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -815,7 +863,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     // has all of the pair, else its partial result for the other CTAs.
     const int my_id = lane < 2 * kWarps ? ids[lane] : -1;
     unsigned int left = __ballot_sync(0xffffffffu, my_id >= 0);
-    int n_slots = 0, slot0_pair = -1, slot1_pair = -1;
+    int n_slots = 0, slot0_pair = -1, slot1_pair = -1, turn = 0;
     while (left) {
         const int pair = ids[__ffs(left) - 1];
         const unsigned int group = __ballot_sync(0xffffffffu, my_id == pair);
@@ -824,9 +872,10 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         const int64_t n = tiles_before(b + 1) - tiles_before(b), begin = first_of(b) + h * n;
         const bool whole = begin >= cta_lo && begin + n <= cta_hi;
         float *to = part + (static_cast<int64_t>(blockIdx.x) * 2 + n_slots) * PS;
-        // a warp for a query head: the entries' weights lane by lane, then the
-        // head's dims over the lanes
-        for (int q = warp; q < r; q += kWarps) {
+        // a warp for a query head of a pair: the entries' weights lane by
+        // lane, then the head's dims over the lanes
+        for (int q = 0; q < r; ++q, turn = turn + 1 == kWarps ? 0 : turn + 1) {
+            if (turn != warp) continue;
             const bool in = group >> lane & 1;
             const float m_e = in ? entry_at(lane)[r * D + q] : -INFINITY;
             const float l_e = in ? entry_at(lane)[r * D + r + q] : 0.f;
@@ -863,30 +912,34 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 
     // Pairs shared with other CTAs: the last one to arrive joins them.
     __syncthreads();
-    if (tid < n_slots) {
-        __threadfence();  // (for the whole CTA, which has met at the barrier)
-        const int pair = tid == 0 ? slot0_pair : slot1_pair, b = pair / c.Hkv, h = pair - b * c.Hkv;
-        const unsigned int arrived = atomicAdd(tickets + pair, 1u);
-        const int64_t n = tiles_before(b + 1) - tiles_before(b), begin = first_of(b) + h * n;
-        const int c0 = cta_of(b, h, n, 0), n_parts = cta_of(b, h, n, n - 1) - c0 + 1;
-        // CTA c0 holds the pair in its last slot: the second one if a pair
-        // that begins before the CTA takes the first
-        bool second = false;
-        const int64_t clo = tile_from(total * c0 / n_ctas);
-        if (clo < begin) {
-            const int rb = row_at(clo);
-            second = (clo - first_of(rb)) % (tiles_before(rb + 1) - tiles_before(rb)) != 0;
+    if (lane < n_slots && warp < 2) {
+        const int pair = lane == 0 ? slot0_pair : slot1_pair;
+        if (warp == 0) {
+            __threadfence();  // (for the whole CTA, which has met at the barrier)
+            arrived_s[lane] = atomicAdd(tickets + pair, 1u);
+            __threadfence();
+        } else {
+            const int b = pair / c.Hkv, h = pair - b * c.Hkv;
+            const int64_t n = tiles_before(b + 1) - tiles_before(b), begin = first_of(b) + h * n;
+            const int c0 = cta_of(b, h, n, 0), n_parts = cta_of(b, h, n, n - 1) - c0 + 1;
+            // CTA c0 holds the pair in its last slot: the second one if a
+            // pair that begins before the CTA takes the first
+            bool second = false;
+            const int64_t clo = place_from(total * c0 / n_ctas).tile;
+            if (clo < begin) {
+                const int rb = row_at(clo);
+                second = (clo - first_of(rb)) % (tiles_before(rb + 1) - tiles_before(rb)) != 0;
+            }
+            join_s[lane] = make_int3(n_parts, c0, second);
         }
-        const bool last = arrived == static_cast<unsigned int>(n_parts - 1);
-        join_s[tid] = make_int3(last ? n_parts : 0, c0, second);
-        if (last) tickets[pair] = 0;  // ready for the next call
-        __threadfence();
     }
     __syncthreads();
     for (int k = 0; k < n_slots; ++k) {
         const int n_parts = join_s[k].x;
-        if (n_parts == 0) continue;
-        const int pair = k == 0 ? slot0_pair : slot1_pair, b = pair / c.Hkv, h = pair - b * c.Hkv;
+        if (arrived_s[k] != static_cast<unsigned int>(n_parts - 1)) continue;
+        const int pair = k == 0 ? slot0_pair : slot1_pair;
+        if (tid == 0) tickets[pair] = 0;  // ready for the next call
+        const int b = pair / c.Hkv, h = pair - b * c.Hkv;
         const float *p0 = part + static_cast<int64_t>(join_s[k].y) * 2 * PS;
         const int skip0 = join_s[k].z ? PS : 0;
         auto part_at = [&](int y) { return p0 + (y == 0 ? skip0 : y * 2 * PS); };
