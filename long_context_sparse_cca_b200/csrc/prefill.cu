@@ -54,7 +54,8 @@
 
 namespace cca {
 
-__device__ unsigned int g_prefill_status;  // kStatusTimeout | kStatusRange
+__device__ unsigned int g_prefill_status;  // kStatusTimeout, kStatusRange, kStatusSeqlens
+__device__ uint4 g_zeros[128 * 128 / 16];  // 128 rows of a box
 
 namespace {
 
@@ -101,6 +102,7 @@ struct Params {
     const int *cu;
     int S;
     int64_t total;
+    int zigzag;             // every other round of the CTAs goes backwards
     int64_t o_row, o_head;
 };
 
@@ -153,13 +155,11 @@ __device__ __forceinline__ Geom geom(int item, int n_blocks, const Params &p, co
             G.hq = item / n_blocks;
             i = item - G.hq * n_blocks;
         } else {
-            // every other round of the CTAs goes backwards: who took the
-            // longest block of one round takes the shortest of the next
-            // (3840 tiles in blocks of 1 to 16 over 148 CTAs: at most 33 a
-            // CTA instead of 39)
-            const int n = gridDim.x, round = item / n;
-            if ((round & 1) && (round + 1) * n <= n_blocks * p.Hq)
-                item = (2 * round + 1) * n - 1 - item;
+            if (p.zigzag) {
+                const int n = gridDim.x, round = item / n;
+                if ((round & 1) && (round + 1) * n <= n_blocks * p.Hq)
+                    item = (2 * round + 1) * n - 1 - item;
+            }
             i = item / p.Hq;
             G.hq = item - i * p.Hq;
         }
@@ -218,6 +218,7 @@ struct Bars {
     uint64_t qh_full[2];
     uint64_t k_full[4], k_empty[4];
     uint64_t v_full[4], v_empty[4];
+    uint64_t raw;  // PK: a tile has landed whose rows behind the end are still to be zeroed
     uint64_t s_full[2];  // S holds half h's scores of its current tile
     uint64_t s_free[2];  // half h has read its S row into registers
     uint64_t p_full[2];
@@ -248,6 +249,16 @@ __device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, Bars *
     const bool ok = wait_bounded(bar, parity, &bars->abort, kWaitLimitNs);
     if (!ok) record_timeout(bars);
     return ok;
+}
+
+// Zeros over the last n rows of a tile, by the copy engine, counted on bar.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int n, uint64_t *bar)
+{
+    using C = Pf<D>;
+    if (n == 0) return;
+    for (int bx = 0; bx < C::NBOX; ++bx)
+        bulk_load(tile + bx * C::BOX_BYTES + (128 - n) * 128, g_zeros, n * 128, bar);
 }
 
 __device__ __forceinline__ float fmax3(float a, float b, float c)
@@ -307,10 +318,14 @@ __device__ __forceinline__ float row_max128(const float (&x)[128])
 // a separate instance, so that the inference kernel is unchanged.
 // HM: item order (geom), a separate instance for the same reason.
 // PK: packed sequences, likewise.  A tile's rows behind the end of its
-// sequence are other sequences' rows or belong to none: their scores are
-// masked by position like every other key's, and their value rows, which
-// P V would multiply by zero weights (0 x NaN = NaN), are set to zero in
-// shared memory.
+// sequence are other sequences' rows or belong to none.  Scores are masked by
+// position as ever; but a value row behind the end meets zero weights
+// (0 x NaN = NaN), and a query row behind it would be turned into fp16 with
+// the others and reported if it does not fit.  So the TMA producer, once such
+// a tile has landed, copies zeros over those rows before it tells anyone.
+// The other roles' loops stay as they are (the zeros written by softmax
+// warps, for tiles with a mask only, cost 4% at 32K; by a warp that looks at
+// every tile, 15%).
 template <int D, bool LSE, bool HM, bool PK>
 __global__ void __launch_bounds__(352, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ,
@@ -349,6 +364,7 @@ __global__ void __launch_bounds__(352, 1)
             mbar_init(&bars->o_bar[h], 1);
             mbar_init(&bars->o_empty[h], 4);
         }
+        mbar_init(&bars->raw, 1);
         mbar_init(&bars->mma_done, 1);
         mbar_init(&bars->mma_done2, 1);
         bars->abort = 0;
@@ -393,17 +409,27 @@ __global__ void __launch_bounds__(352, 1)
     if (warp == 8) {
         // ------------------------------------------------ TMA producer
         if (lane == 0) {
-            uint32_t kc = 0, vc = 0, qc = 0;
+            uint32_t kc = 0, vc = 0, qc = 0, raws = 0;  // raws: phases of `raw`
             bool ok = true;
             for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
                 const Geom G = geom<HM, PK>(item, n_blocks, p, scu, list);
                 if (qc > 0 && !(ok = lane_wait(&bars->q_empty, (qc - 1) & 1, bars))) break;
-                mbar_arrive_expect_tx(&bars->q_full, 2 * C::TILE_BYTES);
+                // (the query rows behind the end matter where they become fp16)
+                const bool q_behind = PK && G.n_core_tiles > 0 && G.t0 + 256 > G.T;
+                uint64_t *q_bar = q_behind ? &bars->raw : &bars->q_full;
+                mbar_arrive_expect_tx(q_bar, 2 * C::TILE_BYTES);
                 for (int hh = 0; hh < 2; ++hh)
                     for (int bx = 0; bx < C::NBOX; ++bx)
                         tma_load_3d(sQ + hh * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ,
-                                    &bars->q_full, bx * 64, G.row0 + G.t0 + hh * 128,
+                                    q_bar, bx * 64, G.row0 + G.t0 + hh * 128,
                                     G.b * p.Hq + G.hq);
+                if (q_behind) {
+                    if (!(ok = lane_wait(&bars->raw, raws++ & 1, bars))) break;
+                    const int n0 = max(0, G.t0 + 128 - G.T), n1 = min(128, G.t0 + 256 - G.T);
+                    mbar_arrive_expect_tx(&bars->q_full, (n0 + n1) * C::NBOX * 128);
+                    zero_rows<D>(sQ, n0, &bars->q_full);
+                    zero_rows<D>(sQ + C::TILE_BYTES, n1, &bars->q_full);
+                }
                 ++qc;
                 const int z = G.b * p.Hkv + G.h;
                 for (int j = 0; j < G.n_tiles; ++j) {
@@ -425,10 +451,17 @@ __global__ void __launch_bounds__(352, 1)
                         const int s = vc % C::VST;
                         if (!(ok = lane_wait(&bars->v_empty[s], ((vc / C::VST) & 1) ^ 1, bars)))
                             break;
-                        mbar_arrive_expect_tx(&bars->v_full[s], C::TILE_BYTES);
+                        const int n_behind = PK ? rows_behind(G, j) : 0;
+                        uint64_t *v_bar = n_behind > 0 ? &bars->raw : &bars->v_full[s];
+                        mbar_arrive_expect_tx(v_bar, C::TILE_BYTES);
                         for (int bx = 0; bx < C::NBOX; ++bx)
                             tma_load_3d(sV + s * C::TILE_BYTES + bx * C::BOX_BYTES, mv,
-                                        &bars->v_full[s], bx * 64, key0, z);
+                                        v_bar, bx * 64, key0, z);
+                        if (n_behind > 0) {
+                            if (!(ok = lane_wait(&bars->raw, raws++ & 1, bars))) break;
+                            mbar_arrive_expect_tx(&bars->v_full[s], n_behind * C::NBOX * 128);
+                            zero_rows<D>(sV + s * C::TILE_BYTES, n_behind, &bars->v_full[s]);
+                        }
                         ++vc;
                     }
                 }
@@ -447,6 +480,7 @@ __global__ void __launch_bounds__(352, 1)
                              kWaitLimitNs);
             }
             if (qc > 0) wait_bounded(&bars->q_full, (qc - 1) & 1, never, kWaitLimitNs);
+            if (PK && raws > 0) wait_bounded(&bars->raw, (raws - 1) & 1, never, kWaitLimitNs);
         }
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------ tcgen05 issuers
@@ -602,23 +636,6 @@ __global__ void __launch_bounds__(352, 1)
                         const int key = key0 + e;
                         if (key < lo || key > hi) x[e] = -INFINITY;
                     }
-                    if (PK && hh == 0 && rows_behind(G, j) > 0) {
-                        // half A's P V is issued first and waits for these
-                        // warps; tiles like this one are masked in every
-                        // half that has rows, so no other tile gets here
-                        // (beside P, in every tile's path, the same code
-                        // cost 4% at 32K)
-                        const uint32_t sv = it % C::VST;
-                        if (!(ok = warp_wait(&bars->v_full[sv], (it / C::VST) & 1, bars))) break;
-                        if (row >= 128 - rows_behind(G, j)) {
-#pragma unroll 1
-                            for (int c = 0; c < C::NBOX * 8; ++c)
-                                *reinterpret_cast<uint4 *>(sV + sv * C::TILE_BYTES +
-                                                           (c >> 3) * C::BOX_BYTES + row * 128 +
-                                                           (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            fence_proxy_async_smem();
-                        }
-                    }
                 }
                 const float m_tile = row_max128(x) * p.scale_log2;
                 float alpha = 1.f;
@@ -688,13 +705,10 @@ __global__ void __launch_bounds__(352, 1)
                     for (int c = row; c < C::TILE_BYTES / 16; c += 128) {
                         const uint4 v = q4[c];
                         uint4 h;
-                        const bool before = over;
                         h.x = pack_f16x2(clamp_f16(bf16_lo(v.x), over), clamp_f16(bf16_hi(v.x), over));
                         h.y = pack_f16x2(clamp_f16(bf16_lo(v.y), over), clamp_f16(bf16_hi(v.y), over));
                         h.z = pack_f16x2(clamp_f16(bf16_lo(v.z), over), clamp_f16(bf16_hi(v.z), over));
                         h.w = pack_f16x2(clamp_f16(bf16_lo(v.w), over), clamp_f16(bf16_hi(v.w), over));
-                        // a query row behind the sequence's end is not reported
-                        if (PK && t0h + ((c >> 3) & 127) >= G.T) over = before;
                         q4[c] = h;
                     }
                     if (over) atomicOr(&g_prefill_status, kStatusRange);
@@ -712,9 +726,15 @@ __global__ void __launch_bounds__(352, 1)
             // before its tensor memory is released
             const float inv = 1.0f / l_run;
             const int64_t orow = (static_cast<int64_t>(G.b) * p.Hq + G.hq) * p.T + t;
-            const bool store = t < G.T;
-            const int64_t oelem =
-                PK ? G.hq * p.o_head + (static_cast<int64_t>(G.row0) + t) * p.o_row : orow * D;
+            bool store = t < G.T;
+            int64_t oelem = orow * D;
+            if constexpr (PK) {  // (found again: registers that hold it meanwhile cost 1%)
+                int again = item;
+                asm volatile("" : "+r"(again));
+                const Geom E = geom<HM, PK>(again, n_blocks, p, scu, list);
+                store = t < E.T;
+                oelem = E.hq * p.o_head + (static_cast<int64_t>(E.row0) + t) * p.o_row;
+            }
             if (LSE && store) p.lse[orow] = (m_run == -INFINITY ? 0.f : m_run) + __log2f(l_run);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -801,6 +821,7 @@ cudaError_t launch_d(const void *Q, const void *K, const void *V, const void *Kc
     p.block_count = p.cu = nullptr;
     p.S = 0;
     p.total = 0;
+    p.zigzag = 0;
     p.o_row = p.o_head = 0;
     int dev = 0, sms = 148, l2 = 0;
     cudaGetDevice(&dev);
@@ -865,6 +886,12 @@ cudaError_t launch_packed_d(const PackedRows &Q, const PackedRows &K, const Pack
     cudaDeviceGetAttribute(&l2, cudaDevAttrL2CacheSize, dev);
     const int64_t most = packed_max_blocks(S, total) * Hq;
     const int grid = static_cast<int>(most < sms ? most : sms);
+    // In a few rounds of blocks, who took the longest block of one round
+    // takes the shortest of the next: 576 blocks of 1 to 16 tiles (8 causal
+    // prompts of 16 heads, d = 64) take 82 us instead of 84.  In many rounds
+    // that evens out by itself, and the order of L2's reuse counts: 2112
+    // blocks (6 prompts, 32 heads, d = 128) take 578 us forwards, 587 so.
+    p.zigzag = most <= 8LL * grid;
     // head by head, as above, when what a query may look far back into (the
     // core rows; for plain causal attention all keys and values) exceeds
     // half the L2

@@ -313,7 +313,7 @@ def test_model_fork_keeps_contents():
 
 # ---- the barrier protocol of the packed attention kernel
 
-def _packed_items(lens, g, w, Hq, cta, grid):
+def _packed_items(lens, g, w, Hq, cta, grid, zigzag=True):
     """Blocks with the most key tiles first, as the kernel deals them:
     (local tiles, core tiles, [tiles that reach behind the sequence])."""
     blocks = sorted(((-(blk + 1), s, n, blk) for s, n in enumerate(lens)
@@ -321,7 +321,7 @@ def _packed_items(lens, g, w, Hq, cta, grid):
     out = []
     for item in range(cta, len(blocks) * Hq, grid):
         k = item // grid
-        if k % 2 and (k + 1) * grid <= len(blocks) * Hq:
+        if zigzag and k % 2 and (k + 1) * grid <= len(blocks) * Hq:
             item = (2 * k + 1) * grid - 1 - item
         _, _, n, blk = blocks[item // Hq]
         t0, tlast = blk * 256, min(blk * 256 + 255, n - 1)
@@ -334,25 +334,30 @@ def _packed_items(lens, g, w, Hq, cta, grid):
     return out
 
 
-def _first_half_softmax(sim, items, VST=2, wait=True):
-    """softmax(0) of the packed kernel: where a tile reaches behind its
-    sequence it waits for the value tile and clears rows before P is ready."""
-    it = 0
+def _producer(sim, items, KST=3, VST=2):
+    """The packed kernel's TMA producer: a value tile that reaches behind its
+    sequence lands on a barrier of the producer's own, and v_full completes
+    with the zeros that are copied over it."""
+    qc = kc = vc = raw = 0
     for nl, nc, behind in items:
+        if qc > 0:
+            yield from sim.wait("q_empty", qc - 1)
+        sim.arrive("q_full")
+        qc += 1
         for j in range(nl + nc):
-            yield from sim.wait("s_full0", it)
-            sim.arrive("s_free0")
-            yield
-            if wait and behind[j]:
-                yield from sim.wait(f"v_full{it % VST}", it // VST)
-            if it > 0:
-                yield from sim.wait("o_bar0", it - 1)
-            sim.arrive("p_full0")
-            if nc > 0 and j == nl - 1:
-                sim.arrive("qh_full0")
-            it += 1
-        yield from sim.wait("o_bar0", it - 1)
-        sim.arrive("o_empty0")
+            if kc >= KST:
+                yield from sim.wait(f"k_empty{kc % KST}", kc // KST - 1)
+            sim.arrive(f"k_full{kc % KST}")
+            kc += 1
+            if vc >= VST:
+                yield from sim.wait(f"v_empty{vc % VST}", vc // VST - 1)
+            if behind[j]:
+                sim.arrive("raw")
+                yield from sim.wait("raw", raw)
+                raw += 1
+                yield
+            sim.arrive(f"v_full{vc % VST}")
+            vc += 1
 
 
 @pytest.mark.parametrize("case", [
@@ -363,11 +368,12 @@ def test_packed_prefill_protocol(case):
     n_items = sum(-(-n // 256) for n in lens) * Hq
     for grid in sorted({1, 2, 3, min(n_items, 148)}):
         for cta in sorted({0, grid - 1, grid // 2}):
-            items = _packed_items(lens, g, w, Hq, cta, grid)
+            items = _packed_items(lens, g, w, Hq, cta, grid, zigzag=grid != 2)
             for seed in range(2):
                 sim = pm.Sim()
                 roles = pm.prefill_roles(sim, [(nl, nc) for nl, nc, _ in items])
-                roles[3] = _first_half_softmax(sim, items)
+                sim.bar("raw")
+                roles[0] = _producer(sim, items)
                 sim.run(roles, seed)
 
 
