@@ -437,6 +437,7 @@ cca_status cca_attn_prefill_packed(const cca_rows *Q, const cca_rows *K, const c
  * count 0 is free.  A full page may belong to several rows
  * (cca_paged_fork); the page a row writes next is its own.
  * page: a power of two, 16 .. 1024.  Hq / Hkv <= 16.  B <= 4096.
+ * raw_cols * page <= 2^31 - 256.
  * core_cols and core_pages may both be 0: a cache of plain causal
  * attention, for w >= raw_cols * page (no window ever ends).
  * The buffers belong to the caller; lens is 8-byte, pools 16-byte aligned.

@@ -91,6 +91,7 @@ cca_status paged_status(const cca_paged_cache *c)
         return CCA_ERR_INVALID_ARG;
     if (c->page < 16 || c->page > 1024 || c->B > 4096 || c->Hq / c->Hkv > 16)
         return CCA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(c->raw_cols) * c->page > kMaxT) return CCA_ERR_UNSUPPORTED;
     const bool core = c->core_cols > 0;
     if (!core && c->w < static_cast<int64_t>(c->raw_cols) * c->page) return CCA_ERR_INVALID_ARG;
     if (!ptr_ok(c->k_raw, true) || !ptr_ok(c->v_raw, true) || !ptr_ok(c->k_core, core) ||

@@ -5,25 +5,29 @@
 // token.
 //
 // Bound by HBM: every attended key and value row is read once, for all r
-// query heads of its key/value head.  Keys are taken in tiles of 16 rows,
-// which lie in one page one behind the other.  The tiles of all (row,
+// query heads of its key/value head (8 rows of 65K tokens, 32 heads, d = 128:
+// 665 MB in 124 us, 5.4 TB/s; while all warps stream, 6.4).  Keys are taken
+// in tiles of 8 KB of keys and values (16 rows, or 32 of d = 64), whose rows
+// lie 16 by 16 in one page, one behind the other.  The tiles of all (row,
 // key/value head) pairs form one list; every CTA, and in it every warp, gets
 // an equal stretch of it, whatever the rows' lengths, found on the device
-// from lens.  A warp keeps one tile of keys and one of values in registers
-// and asks for the next ones as soon as the present ones are used.
+// from lens.  Each warp copies its tiles into a ring of its own in shared
+// memory, two or three deep (cp.async: some 100 KB in flight for an SM
+// without registers, and no barrier between warps; 16-byte loads into
+// registers reached 80% of that).
 //
 // A tile's arithmetic runs on mma.m16n8k16 (the queries of a pair are at
 // most 16 rows; tcgen05 wants 64 or 128 of them): S = Q K^T, then O += P V.
 // Both contractions may take their index in any order, so the operands are
-// read from the cache as 16-byte pieces of rows straight into fragments:
-//   S: thread (i = lane / 4, j = lane % 4) holds dims 32 c + 8 j .. + 7 of
-//      keys i and i + 8 (c = 0 .. D/32 - 1), and the same dims of query i;
+// read from the ring as 16-byte pieces of rows straight into fragments:
+//   S: thread (i = lane / 4, j = lane % 4) holds dims 64 h + 16 j .. + 15 of
+//      keys i and i + 8, and the same dims of query i;
 //   O: dims 64 h + 8 i .. + 7 of keys 2j, 2j + 1, 2j + 8, 2j + 9; two keys'
 //      rows interleave into the pairs of keys that a fragment holds.
 // Raw rows are bf16 and core rows fp16, and both operands of a product have
 // one type: for core tiles the query row is rounded to fp16 after a power of
-// two brought its largest entry to 2^13 .. 2^14 (exact but for entries 2^-27
-// below that one).  P is split into two numbers of the tile's type, P =
+// two brought its largest entry to 2^13 .. 2^14 (exact but for entries below
+// 2^-27 of that one).  P is split into two numbers of the tile's type, P =
 // P_hi + P_lo up to 2^-17, so that P V is as good as with fp32 weights; for
 // up to 8 query heads P_lo takes the fragment rows that are free, and costs
 // nothing.  Scores, running maximum and sum, and outputs are fp32.
@@ -31,6 +35,10 @@
 // Stretches that share a pair are joined in shared memory within a CTA, and
 // across CTAs by the last one that arrives at the pair (a ticket), always in
 // the order of the list: results do not depend on the order of arrival.
+// What is left beside the streaming is latency: of 31 us for 16 rows of up
+// to 32K tokens (101 MB), 2 are for the list, 5 until the first tile, 2 for
+// each join.  (Smaller stretches handed out as CTAs get done: 190 us instead
+// of 130 for the 8 rows; a stretch's begin and end take 8 us.)
 #include <type_traits>
 
 #include "paged.cuh"
@@ -166,10 +174,13 @@ __device__ __forceinline__ void put8(void *o_t, int o_f32, int64_t at, const flo
 constexpr int kCore = 1 << 12, kNewest = 1 << 13, kFirst = 1 << 14, kEnds = 1 << 15,
               kPage = 1 << 16;
 
-// What a pair costs a warp beside its tiles, and what a pooling does, in
-// tiles.
+// What a pair costs a warp beside its tiles (queries, output, page numbers),
+// and what a pooling does, in tiles: by the timeline of a batch of 64 rows of
+// 1 to 16K tokens, where CTAs with many short rows took twice as long as the
+// others without (72 us instead of 58).
 constexpr int kPairTiles = 3, kPoolTiles = 4;
 
+// WIDE: 9 to 16 query heads for a key/value head; STEP: cca_paged_step.
 template <int D, int WARPS, int STAGES, bool WIDE, bool STEP>
 __global__ void __launch_bounds__(WARPS * 32, 1)
     paged_decode_kernel(PagedView c, const uint16_t *__restrict__ q_t,
@@ -1045,6 +1056,9 @@ cudaError_t launch_paged_decode(const cca_paged_cache &c, int layer, const void 
     const integral_constant<int, 2> n2{};
     const std::true_type wide{};
     const std::false_type narrow{};
+    // 12 warps, as many as 168 registers allow, or 8 where more than 8 heads
+    // or the room ask for it (8 with a ring of 3: the 8 rows above in 135 us
+    // instead of 133).
     if (c.d == 128) {
         if (r > 8) return run(d128, n8, n2, wide);
         if (fits(12, 2)) return run(d128, n12, n2, narrow);

@@ -264,6 +264,10 @@ CASES = [  # Hq, Hkv, d, g, w, page, prompts, core pages?
     (4, 1, 64, 16, ALL, 16, [300, 16, 1, 700], False),
     (4, 4, 128, 16, ALL, 32, [33, 32, 31, 2000], True),
     (32, 2, 64, 256, 300, 16, [2500, 255, 256, 511], True),
+    (12, 1, 128, 16, 64, 16, [200, 257, 1, 79], True),
+    (9, 1, 64, 32, 40, 16, [500, 31, 1, 64], True),
+    (8, 1, 128, 16, 64, 32, [1500, 257, 2, 80], True),
+    (14, 2, 128, 17, 50, 16, [333, 17, 34, 800], True),
 ]
 
 
@@ -278,6 +282,52 @@ def test_steps_match_oracle(cca, case):
     for i in range(2 * min(g, 16) + 2):
         r.step(check=i < 2 or i % 5 == 0)
     assert cca.cca_device_status() == cca.CCA_OK
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(4096, 2, 2, 64), (3000, 8, 1, 128), (700, 16, 1, 128),
+                                        (1000, 3, 1, 64)])
+def test_many_rows(cca, B, Hq, Hkv, d):
+    """Batches whose list takes the room of a ring's stage or of warps; rows
+    of 0 to 60 tokens, every one against its own attention in fp64 (w = 0 and
+    g = 4: core rows of all groups but the last)."""
+    import torch
+    g, w, page = 4, 0, 16
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 61, size=B)
+    total = int(lens.sum())
+    q, k, v, cu = packed_inputs(lens.tolist(), Hq, Hkv, d, B)
+    Q, K, V = (to_cuda(x) for x in (q, k, v))
+    c = cca.PagedCache(B, Hq, Hkv, d, g, w, page, 2 * B, 2 * B, max_len=64)
+    cca.cca_paged_reserve(c, _i64(lens.tolist()))
+    half = B // 2  # (a call takes up to 8192 sequences; two calls here)
+    for a, b in ((0, half), (half, B)):
+        lo, hi = int(cu[a]), int(cu[b])
+        x = [t[:, lo:hi] for t in (Q, K, V)]
+        cu_d = _i32((cu[a:b + 1] - lo).tolist())
+        Kc, Vc = cca.cca_pool_packed(*x, cu_d, g)
+        cca.cca_paged_fill(c, x[1], x[2], Kc, Vc, cu_d, _i32(list(range(a, b))))
+    qt = to_cuda(synth.random_bf16((B, Hq, d), 3 * B))
+    o = cca.cca_attn_decode_paged(c, qt, out_dtype=torch.float32)
+    assert cca.cca_device_status() == cca.CCA_OK
+    # the definition, all rows at once: groups before the window's, then it
+    f = torch.float64
+    n = torch.from_numpy(lens).cuda()
+    ws = (n - 1).clamp(min=0) // g * g
+    p = torch.arange(64, device="cuda")
+    first = torch.from_numpy(cu[:-1].astype(np.int64)).cuda()
+    at = (first[:, None] + p).clamp(max=max(total - 1, 0))
+    Kr, Vr = (t[:, at].to(f) for t in (K, V))                       # [Hkv, B, 64, d]
+    qg = Q[:, at[:, g - 1::g]].to(f).view(Hkv, Hq // Hkv, B, 16, d)  # the groups' last queries
+    kg, vg = (t.view(Hkv, B, 16, g, d) for t in (Kr, Vr))
+    a = torch.softmax(torch.einsum("hrbjd,hbjgd->hrbjg", qg, kg) / d ** 0.5, -1).mean(1)
+    Kc, Vc = (torch.einsum("hbjg,hbjgd->hbjd", a, t) for t in (kg, vg))
+    keys, vals = torch.cat([Kc, Kr], 2), torch.cat([Vc, Vr], 2)
+    seen = torch.cat([p[:16] < (ws // g)[:, None],
+                      (p >= ws[:, None]) & (p < n[:, None])], 1)
+    s = torch.einsum("bhrd,hbkd->bhrk", qt.to(f).view(B, Hkv, -1, d), keys) / d ** 0.5
+    s = s.masked_fill(~seen[:, None, None], -float("inf"))
+    ref = torch.einsum("bhrk,hbkd->bhrd", torch.nan_to_num(torch.softmax(s, -1)), vals)
+    assert_close(o, ref.reshape(B, Hq, d).cpu().numpy(), None, "o")
 
 
 def test_steps_from_an_empty_prompt(cca):

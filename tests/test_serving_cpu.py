@@ -124,7 +124,7 @@ BAD_CACHES = [
     (dict(layers=0), BAD), (dict(B=0), BAD), (dict(B=4097), NOT_HERE), (dict(Hq=3), BAD),
     (dict(Hq=64), NOT_HERE), (dict(d=96), NOT_HERE), (dict(g=0), BAD), (dict(g=257), NOT_HERE),
     (dict(w=-1), BAD), (dict(page=24), BAD), (dict(page=0), BAD), (dict(page=8), NOT_HERE),
-    (dict(page=2048), NOT_HERE), (dict(raw_cols=0), BAD), (dict(raw_pages=0), BAD),
+    (dict(page=2048), NOT_HERE), (dict(raw_cols=1 << 21, page=1024), NOT_HERE), (dict(raw_cols=0), BAD), (dict(raw_pages=0), BAD),
     (dict(core_cols=0), BAD), (dict(core_pages=0), BAD), (dict(core_cols=-1), BAD),
     (dict(core_cols=0, core_pages=0), BAD),  # a window that ends needs core rows
     (dict(k_raw=0), BAD), (dict(v_core=_at(21) + 8), BAD), (dict(lens=_at(28) + 4), BAD),
