@@ -401,8 +401,9 @@ cca_status cca_pool_packed(const cca_rows *Q, const cca_rows *K, const cca_rows 
                            const int32_t *cu, void *Kc, void *Vc, int S, int Hq, int Hkv,
                            int64_t total, int d, int g, cudaStream_t stream);
 
-/* Bytes of device workspace cca_attn_prefill_packed needs (0 for an invalid
- * shape): the order in which it takes the sequences' query blocks. */
+/* Bytes of device workspace cca_attn_prefill_packed needs, for the order in
+ * which it takes the sequences' query blocks (0 for up to 64 sequences with up
+ * to 256 blocks, total / 256 + S, and for an invalid shape). */
 size_t cca_packed_workspace_bytes(int S, int64_t total);
 
 /*
@@ -410,9 +411,12 @@ size_t cca_packed_workspace_bytes(int S, int64_t total);
  * sequence's causal attention over its own core rows (Kc, Vc from
  * cca_pool_packed) and its own window.  w >= total is plain causal
  * attention: no core row is seen, Kc and Vc may be NULL.
- * workspace: cca_packed_workspace_bytes(S, total) bytes, 256-byte aligned;
- * its contents need no initialisation.  Calls sharing a workspace must not
- * overlap on the GPU.
+ * workspace: cca_packed_workspace_bytes(S, total) bytes, 256-byte aligned
+ * (may be NULL for 0); its contents need no initialisation.  Calls sharing a
+ * workspace must not overlap on the GPU.
+ * Sequences are isolated from one another whatever they hold.  Within one,
+ * as in cca_attn_prefill, a value row that is not finite may reach the
+ * outputs of earlier rows whose 128-key tile it lies in.
  */
 cca_status cca_attn_prefill_packed(const cca_rows *Q, const cca_rows *K, const cca_rows *V,
                                    const void *Kc, const void *Vc, const int32_t *cu,
@@ -441,6 +445,7 @@ cca_status cca_attn_prefill_packed(const cca_rows *Q, const cca_rows *K, const c
  * core_cols and core_pages may both be 0: a cache of plain causal
  * attention, for w >= raw_cols * page (no window ever ends).
  * The buffers belong to the caller; lens is 8-byte, pools 16-byte aligned.
+ * Rows of a page that hold no token, and free pages, may hold anything.
  * A new cache: tables filled with -1, counts and lens with 0.
  *
  * The calls below read lens and tables on the device: a sequence of them can

@@ -653,10 +653,10 @@ def cca_pool_packed(Q, K, V, cu, g: int, Kc=None, Vc=None, stream=None):
     bf, dev = torch.bfloat16, _device(Q, "Q")
     Hq, Hkv, total, d = _packed_shapes(Q, K)
     shape = (Hkv, total // int(g) if g > 0 else 0, d)
-    if Kc is None:
-        Kc = Q.new_empty(shape, dtype=torch.float16)
-    if Vc is None:
-        Vc = Q.new_empty(shape, dtype=torch.float16)
+    if Kc is None and Vc is None:
+        Kc, Vc = Q.new_empty((2, *shape), dtype=torch.float16).unbind(0)
+    elif Kc is None or Vc is None:
+        raise ValueError("give both Kc and Vc, or neither")
     _check(lib().cca_pool_packed(
         _rows(Q, "Q", (Hq, total, d), bf, dev), _rows(K, "K", (Hkv, total, d), bf, dev),
         _rows(V, "V", (Hkv, total, d), bf, dev), _offsets(cu, dev),
@@ -690,11 +690,16 @@ def cca_attn_prefill_packed(Q, K, V, Kc, Vc, cu, g: int, w: int, O=None, out_dty
             O = Q.new_empty((total, Hq, d), dtype=dt).transpose(0, 1)
         else:
             O = Q.new_empty((Hq, total, d), dtype=dt)
-    if workspace is None:
-        workspace = Q.new_empty(max(cca_packed_workspace_bytes(S, total), 256),
-                                dtype=torch.uint8)
-        if stream is not None:  # freed on return: not before the work on that stream is done
-            workspace.record_stream(stream)
+    ws, nbytes = None, 0
+    if workspace is not None:
+        ws, nbytes = _here(workspace, "workspace", dev), workspace.numel()
+    elif S > 0:
+        nbytes = lib().cca_packed_workspace_bytes(S, total)
+        if nbytes:
+            workspace = Q.new_empty(nbytes, dtype=torch.uint8)
+            ws = workspace.data_ptr()
+            if stream is not None:  # freed on return: not before that stream's work is done
+                workspace.record_stream(stream)
     core = (Hkv, total // int(g) if g > 0 else 0, d)
     _check(lib().cca_attn_prefill_packed(
         _rows(Q, "Q", (Hq, total, d), bf, dev), _rows(K, "K", (Hkv, total, d), bf, dev),
@@ -702,8 +707,7 @@ def cca_attn_prefill_packed(Q, K, V, Kc, Vc, cu, g: int, w: int, O=None, out_dty
         None if Kc is None else _tensor(Kc, "Kc", core, torch.float16, dev),
         None if Vc is None else _tensor(Vc, "Vc", core, torch.float16, dev), _offsets(cu, dev),
         _rows(O, "O", (Hq, total, d), O.dtype, dev), _odtype(O.dtype), S, Hq, Hkv, total, d, int(g),
-        int(w), _here(workspace, "workspace", dev), workspace.numel(),
-        _raw_stream(stream, dev)), "cca_attn_prefill_packed")
+        int(w), ws, nbytes, _raw_stream(stream, dev)), "cca_attn_prefill_packed")
     return O
 
 
@@ -805,7 +809,8 @@ class PagedCache:
     @classmethod
     def from_state_dict(cls, state: dict, device="cuda") -> "PagedCache":
         """A cache on ``device`` holding what ``state_dict`` saved."""
-        return cls.from_tensors(*(state[n].to(device, copy=True) for n in cls._TENSORS), **state["shape"])
+        return cls.from_tensors(*(state[n].to(device, copy=True) for n in cls._TENSORS),
+                                **state["shape"])
 
     _TENSORS = ("core_table", "raw_table", "core_ref", "raw_ref", "lens", "k_core", "v_core",
                 "k_raw", "v_raw")
@@ -865,7 +870,9 @@ def cca_paged_fill(cache: PagedCache, K, V, Kc, Vc, cu, rows, layer: int = 0,
 def cca_attn_decode_paged(cache: PagedCache, q_t, layer: int = 0, o_t=None, out_dtype=None,
                           workspace=None, stream=None):
     """Attention of the newest token of every row: q_t [B,Hq,d] -> o_t
-    [B,Hq,d]; free rows get zeros.  Capturable in a CUDA graph."""
+    [B,Hq,d]; free rows get zeros.  Capturable in a CUDA graph.  A workspace
+    other than the cache's own (for calls at the same time) must have been
+    zero-filled before its first use."""
     torch, dev = _torch(), _device(cache.tables, "cache")
     shape = cache.q_shape
     if o_t is None:
@@ -873,7 +880,8 @@ def cca_attn_decode_paged(cache: PagedCache, q_t, layer: int = 0, o_t=None, out_
     _check(lib().cca_attn_decode_paged(
         cache.struct, int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16, dev),
         _tensor(o_t, "o_t", shape, o_t.dtype, dev), _odtype(o_t.dtype),
-        *_paged_workspace(cache, workspace, dev), _raw_stream(stream, dev)), "cca_attn_decode_paged")
+        *_paged_workspace(cache, workspace, dev), _raw_stream(stream, dev)),
+        "cca_attn_decode_paged")
     return o_t
 
 

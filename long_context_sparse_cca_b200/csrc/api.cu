@@ -504,6 +504,7 @@ cca_status cca_pool_packed(const cca_rows *Q, const cca_rows *K, const cca_rows 
 size_t cca_packed_workspace_bytes(int S, int64_t total)
 {
     if (S < 1 || S > CCA_MAX_SEQS || total < 0 || total > kMaxT) return 0;
+    if (cca::packed_inline(S, total)) return 0;
     return 256 + 16 * static_cast<size_t>(cca::packed_max_blocks(S, total));
 }
 
@@ -522,9 +523,12 @@ cca_status cca_attn_prefill_packed(const cca_rows *Q, const cca_rows *K, const c
     cca::PackedRows q, k, v, o;
     if (!rows_ok(Q, Hq, total, d, 8, 16, false, q) || !rows_ok(K, Hkv, total, d, 8, 16, false, k) ||
         !rows_ok(V, Hkv, total, d, 8, 16, false, v) || !rows_ok(O, Hq, total, d, 16, 32, true, o) ||
-        !ptr_ok(Kc, core) || !ptr_ok(Vc, core) || !aligned_to(workspace, 256) ||
-        workspace_bytes < cca_packed_workspace_bytes(S, total))
+        !ptr_ok(Kc, core) || !ptr_ok(Vc, core))
         return CCA_ERR_INVALID_ARG;
+    const size_t need = cca_packed_workspace_bytes(S, total);
+    if (need > 0 && (!aligned_to(workspace, 256) || workspace_bytes < need))
+        return CCA_ERR_INVALID_ARG;
+    workspace_bytes = need;
     if (cca::packed_max_blocks(S, total) * Hq > INT32_MAX) return CCA_ERR_UNSUPPORTED;
     const size_t out = rows_bytes(o, Hq, total, d, o_dtype == CCA_F32 ? 4 : 2);
     const size_t nc = core ? size_t(Hkv) * m * d * 2 : 0, ncu = sizeof(int) * (S + 1);

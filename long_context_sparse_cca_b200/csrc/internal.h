@@ -93,6 +93,14 @@ struct PackedRows {
     int64_t row, head;
 };
 inline int64_t packed_max_blocks(int S, int64_t total) { return total / 256 + S; }
+// Up to so many sequences and query blocks every CTA of the attention kernel
+// orders the blocks by itself, beyond that a kernel of its own does.  (That
+// kernel takes 3 us; 64 sequences and 256 blocks fit beside D = 128's tiles.)
+constexpr int kInlineSeqs = 64, kInlineBlocks = 256;
+inline bool packed_inline(int S, int64_t total)
+{
+    return S <= kInlineSeqs && packed_max_blocks(S, total) <= kInlineBlocks;
+}
 cudaError_t launch_packed_plan(const int *cu, int S, int64_t total, int g, int4 *blocks,
                                int *count, cudaStream_t s);
 size_t pool_packed_smem(int S, int r, int g);

@@ -96,9 +96,10 @@ __global__ void __launch_bounds__(kPoolWarps * 32, G > 0 && D * G <= 2048 ? 3 : 
             if (next >= 0)
                 for (int i = lane; i < g * LINES; i += 32) {
                     const int64_t row = next + i / LINES;
-                    const int e = i % LINES * 64;
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(k + h_next * K.head + row * K.row + e));
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(v + h_next * V.head + row * V.row + e));
+                    const uint16_t *kl = k + h_next * K.head + row * K.row + i % LINES * 64;
+                    const uint16_t *vl = v + h_next * V.head + row * V.row + i % LINES * 64;
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(kl));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(vl));
                 }
         }
         uint16_t *kc = Kc + gid * D, *vc = Vc + gid * D;
@@ -117,7 +118,8 @@ __global__ void __launch_bounds__(kPoolWarps * 32, G > 0 && D * G <= 2048 ? 3 : 
         auto qrow = [&](int i) { return Qb + i * Q.head; };
         bool over;
         if constexpr (G > 0)
-            over = pool_group_warp_fast<D, G, false>(krow, vrow, qrow, r, scale_log2, scratch, kc, vc);
+            over = pool_group_warp_fast<D, G, false>(krow, vrow, qrow, r, scale_log2, scratch, kc,
+                                                     vc);
         else
             over = pool_group_warp<D>(krow, vrow, qrow, r, g, scale_log2, scratch, kc, vc);
         if (over && lane == 0) atomicOr(&g_packed_status, kStatusRange);

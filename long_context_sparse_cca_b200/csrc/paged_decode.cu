@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         const int id = lane < n_tiles ? page_at(c.raw_table, b, c.raw_cols,
                                                 ((tile0 + lane) * kPart) >> c.shift, c.raw_pages)
                                       : 0;
-        const int out = ends ? page_at(c.core_table, b, c.core_cols, j >> c.shift, c.core_pages) : 0;
+        const int out =
+            ends ? page_at(c.core_table, b, c.core_cols, j >> c.shift, c.core_pages) : 0;
         const int page = __shfl_sync(0xffffffffu, id, n_tiles - 1);
         // (count 1: the page is the row's own)
         const bool mine = page >= 0 && __ldg(c.raw_ref + page) == 1;
@@ -393,7 +394,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                 copy_rows(ring_s + (slot + i) * P::ROWS,
                           (v ? c.v_raw : c.k_raw) +
                               page_row<D>(pg, h, c.Hkv, c.shift, static_cast<int>(p) & mask),
-                          v ? vin : kin, i0 + i == 0 ? skip : 0, thi, p + thi == t + 1 ? thi - 1 : -1);
+                          v ? vin : kin, i0 + i == 0 ? skip : 0, thi,
+                          p + thi == t + 1 ? thi - 1 : -1);
             }
             commit();
         };
@@ -502,7 +504,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
     // yet among those that it sees.  The pairs go round the CTAs, the last
     // ones first, which have no tiles when there are few.
     const int64_t pairs = static_cast<int64_t>(c.B) * c.Hkv;
-    const int64_t pair0 = kCtas - 1 - static_cast<int>(blockIdx.x) + kCtas * static_cast<int64_t>(warp);
+    const int64_t pair0 =
+        kCtas - 1 - static_cast<int>(blockIdx.x) + kCtas * static_cast<int64_t>(warp);
     if (STEP) {  // groups that this warp is going to pool
         int pools = 0;
         for (int64_t pair = pair0; pair < pairs; pair += kCtas * kWarps)

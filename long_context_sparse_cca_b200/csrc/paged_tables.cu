@@ -34,7 +34,10 @@ struct TablesView {
     int B, g, w, shift;
 };
 
-__device__ __forceinline__ void report(unsigned int bits) { atomicOr(&g_paged_tables_status, bits); }
+__device__ __forceinline__ void report(unsigned int bits)
+{
+    atomicOr(&g_paged_tables_status, bits);
+}
 
 // Exclusive sums over the block (kThreads threads) of each thread's x;
 // total: the sums of all.  One barrier; `room` is used again only after

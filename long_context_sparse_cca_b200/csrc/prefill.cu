@@ -62,11 +62,6 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
 constexpr float kRescaleThreshold = 15.0f;  // log2 units: P stays <= 2^15 (fp16 range)
 
-// Packed sequences: up to so many sequences and query blocks every CTA
-// orders the blocks by itself, beyond that a kernel of its own does.  (The
-// kernel takes 3 us; 64 sequences and 256 blocks fit beside D = 128's tiles.)
-constexpr int kInlineSeqs = 64, kInlineBlocks = 256;
-
 template <int D>
 struct Pf {
     static constexpr int NBOX = D / 64;          // 64-column swizzled boxes
@@ -916,7 +911,7 @@ cudaError_t launch_prefill_packed(const PackedRows &Q, const PackedRows &K, cons
 {
     int *count = static_cast<int *>(workspace);
     int4 *blocks = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + 256);
-    if (S <= kInlineSeqs && packed_max_blocks(S, total) <= kInlineBlocks) {
+    if (packed_inline(S, total)) {
         count = nullptr;
         blocks = nullptr;
     } else {

@@ -29,6 +29,11 @@ def cca():
     return m
 
 
+def _i32(x):
+    import torch
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
 def _layout(x, layout):
     """[H, total, d] in one of the memory orders that occur."""
     import torch
@@ -206,3 +211,43 @@ def test_packed_stream_argument(cca):
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(O, O2) and torch.equal(Kc, Kc2)
     assert to_f64(O).shape == (2, 700, 128)
+
+
+def test_nothing_to_do(cca):
+    """No rows at all, and rows that no sequence owns: outputs stay as they
+    were."""
+    import torch
+    Q, K = (torch.zeros((h, 0, 64), dtype=torch.bfloat16, device="cuda") for h in (4, 2))
+    none = _i32([0, 0])
+    Kc, Vc = cca.cca_pool_packed(Q, K, K, none, 16)
+    assert Kc.shape == Vc.shape == (2, 0, 64)
+    assert cca.cca_attn_prefill_packed(Q, K, K, Kc, Vc, none, 16, 64).shape == (4, 0, 64)
+    Q, K = (torch.full((h, 300, 64), float("nan"), dtype=torch.bfloat16, device="cuda")
+            for h in (4, 2))
+    for cu in ([0, 0, 0], [300, 300], [17, 17, 17, 17]):
+        Kc, Vc = cca.cca_pool_packed(Q, K, K, _i32(cu), 16)
+        assert bool((Kc == 0).all()) and bool((Vc == 0).all())
+        O = torch.full_like(Q, 3.0)
+        cca.cca_attn_prefill_packed(Q, K, K, Kc, Vc, _i32(cu), 16, 64, O=O)
+        assert bool((O == 3).all())
+    assert cca.cca_device_status() == cca.CCA_OK
+
+
+@pytest.mark.parametrize("S", [64, 65])
+def test_block_order_by_every_cta_or_by_a_kernel(cca, S):
+    """On both sides of the border the same result, bit for bit, as one
+    sequence after the other."""
+    import torch
+    rng = np.random.default_rng(S)
+    lens = rng.integers(1, 700, size=S)
+    lens[0] = 900
+    q, k, v, cu = packed_inputs(lens.tolist(), 2, 1, 64, S)
+    assert (cca.cca_packed_workspace_bytes(S, q.shape[1]) > 0) == (S > 64)
+    Q, K, V = (to_cuda(x) for x in (q, k, v))
+    Kc, Vc = cca.cca_pool_packed(Q, K, V, _i32(cu.tolist()), 16)
+    O = cca.cca_attn_prefill_packed(Q, K, V, Kc, Vc, _i32(cu.tolist()), 16, 64)
+    for s in range(0, S, 7):
+        a, b = int(cu[s]), int(cu[s + 1])
+        x = [t[None, :, a:b].contiguous() for t in (Q, K, V)]
+        assert torch.equal(O[:, a:b], cca.cca_attn_prefill(*x, *cca.cca_pool(*x, 16), 16, 64)[0])
+    assert cca.cca_device_status() == cca.CCA_OK

@@ -446,6 +446,25 @@ def test_pages_scattered_over_a_large_pool(cca):
     assert torch.equal(*outs)
 
 
+def test_two_attentions_at_once(cca):
+    """Two streams read one cache, each with a workspace of its own."""
+    import torch
+    r = Rows(cca, 3, 8, 2, 128, 16, 64, 16, 3000)
+    r.prompts([0, 1, 2], [2900, 1500, 64])
+    qs = [to_cuda(synth.random_bf16((3, 8, 128), 700 + i)) for i in range(2)]
+    want = [cca.cca_attn_decode_paged(r.c, q) for q in qs]
+    ws = [torch.zeros_like(r.c.workspace) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        got = [cca.cca_attn_decode_paged(r.c, q, workspace=x, stream=s)
+               for q, x, s in zip(qs, ws, streams)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert cca.cca_device_status() == cca.CCA_OK
+
+
 # ---------------------------------------------------------------- refusals on the device
 
 def test_fill_leaves_out_what_does_not_fit(cca):

@@ -70,7 +70,7 @@ def test_pool_packed_refusals(L):
 
 
 def _attn(L, q=None, k=None, v=None, o=None, Kc=_at(4), Vc=_at(5), S=2, Hq=4, Hkv=2, total=300,
-          d=128, g=16, w=64, cu=_at(6), dt=0, ws=_at(9), n=None):
+          d=128, g=16, w=64, cu=_at(6), dt=0, ws=_at(9), n=None):  # S = 2: no workspace
     n = L.cca_packed_workspace_bytes(S, total) if n is None else n
     return L.cca_attn_prefill_packed(q or _rows(1), k or _rows(2), v or _rows(3), P(Kc), P(Vc),
                                      P(cu), o or _rows(7), dt, S, Hq, Hkv, total, d, g, w, P(ws),
@@ -92,20 +92,23 @@ def test_attn_prefill_packed_refusals(L):
     assert _attn(L, o=_rows(7, row=128, head=256)) == BAD
     assert _attn(L, o=_rows(1)) == BAD                    # in place of Q
     assert _attn(L, o=_rows(4)) == BAD                    # on the core rows
-    assert _attn(L, ws=_at(9) + 128) == BAD
-    assert _attn(L, ws=0) == BAD
-    assert _attn(L, n=L.cca_packed_workspace_bytes(2, 300) - 1) == BAD
-    assert _attn(L, ws=_at(7)) == BAD                     # workspace on the output
-    assert _attn(L, ws=_at(6)) == BAD                     # ... on the offsets
+    assert _attn(L, S=65, ws=_at(9) + 128) == BAD
+    assert _attn(L, S=65, ws=0) == BAD
+    assert _attn(L, S=65, n=L.cca_packed_workspace_bytes(65, 300) - 1) == BAD
+    assert _attn(L, S=65, ws=_at(7)) == BAD               # workspace on the output
+    assert _attn(L, S=65, ws=_at(6)) == BAD               # ... on the offsets
     assert _attn(L, total=0, q=_rows(1, data=0), o=_rows(7, data=0), Kc=0, ws=0) == cca.CCA_OK
 
 
 def test_packed_workspace_bytes(L):
     size = L.cca_packed_workspace_bytes
     assert size(0, 100) == size(8193, 100) == size(1, -1) == 0
-    assert 0 < size(1, 0) < size(1, 100000) < size(8192, 100000)
-    # a pair of 16 bytes for every block that S sequences of `total` rows can have
-    for lens in ([1] * 100, [257, 1, 0, 300], [0, 0], [512, 511, 513]):
+    # none while each CTA orders the blocks by itself
+    assert size(1, 0) == size(64, 192 * 256 + 255) == 0
+    assert size(65, 0) > 0 and size(64, 193 * 256) > 0
+    assert 0 < size(1, 100000) < size(8192, 100000)
+    # then 16 bytes for every block that S sequences of `total` rows can have
+    for lens in ([1] * 100, [257, 1, 0, 300] * 20, [0] * 70, [512, 511, 513] * 50, [70000, 3]):
         blocks = sum(-(-n // 256) for n in lens)
         assert size(len(lens), sum(lens)) >= 256 + 16 * blocks
 
@@ -124,7 +127,8 @@ BAD_CACHES = [
     (dict(layers=0), BAD), (dict(B=0), BAD), (dict(B=4097), NOT_HERE), (dict(Hq=3), BAD),
     (dict(Hq=64), NOT_HERE), (dict(d=96), NOT_HERE), (dict(g=0), BAD), (dict(g=257), NOT_HERE),
     (dict(w=-1), BAD), (dict(page=24), BAD), (dict(page=0), BAD), (dict(page=8), NOT_HERE),
-    (dict(page=2048), NOT_HERE), (dict(raw_cols=1 << 21, page=1024), NOT_HERE), (dict(raw_cols=0), BAD), (dict(raw_pages=0), BAD),
+    (dict(page=2048), NOT_HERE), (dict(raw_cols=1 << 21, page=1024), NOT_HERE),
+    (dict(raw_cols=0), BAD), (dict(raw_pages=0), BAD),
     (dict(core_cols=0), BAD), (dict(core_pages=0), BAD), (dict(core_cols=-1), BAD),
     (dict(core_cols=0, core_pages=0), BAD),  # a window that ends needs core rows
     (dict(k_raw=0), BAD), (dict(v_core=_at(21) + 8), BAD), (dict(lens=_at(28) + 4), BAD),
@@ -386,6 +390,7 @@ def test_packed_blocks_places():
         lens = rng.integers(0, rng.choice([2, 300, 2000]), size=S)
         lead, trail = rng.integers(0, 600, size=2)
         cu = lead + np.concatenate([[0], np.cumsum(lens)])
-        slots = [int(cu[s]) // 256 + s + blk for s in range(S) for blk in range(-(-int(lens[s]) // 256))]
+        slots = [int(cu[s]) // 256 + s + blk
+                 for s in range(S) for blk in range(-(-int(lens[s]) // 256))]
         assert len(set(slots)) == len(slots)
         assert not slots or max(slots) < (int(cu[-1]) + int(trail)) // 256 + S
