@@ -18,22 +18,6 @@ struct PagedView {
     int64_t longest;  // longest row the tables take
 };
 
-// What a row of L tokens holds and sees.
-struct PagedRow {
-    int64_t t;       // newest token
-    int64_t ws;      // its window's first token
-    int64_t n_core;  // core rows it sees (groups before the window)
-};
-
-__host__ __device__ __forceinline__ PagedRow paged_row(int64_t len, int g, int w)
-{
-    PagedRow r;
-    r.t = len - 1;
-    r.ws = len > 0 ? window_start(len - 1, g, w) : 0;
-    r.n_core = r.ws / g;
-    return r;
-}
-
 // Page-table columns of a row of L tokens: raw [raw_lo, raw_hi), core
 // [0, core_hi).
 struct PagedCols {

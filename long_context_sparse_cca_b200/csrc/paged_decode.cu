@@ -134,7 +134,9 @@ __device__ __forceinline__ RowTiles row_tiles(const PagedView &c, int b, bool &o
     const int64_t len = __ldg(c.lens + b);
     over = len > c.longest;  // a row longer than its table is taken as free
     r.len = over || len < 0 ? 0 : len;
-    const int64_t past = r.len - 1 - c.w;  // as paged_row, but for the 32-bit division
+    // groups before the window of token t: max(t - w, 0) / g, in 32 bits where
+    // they do (a 64-bit division takes a hundred instructions)
+    const int64_t past = r.len - 1 - c.w;
     if (past < c.g)
         r.n_core = 0;
     else if (past >> 32 == 0)
