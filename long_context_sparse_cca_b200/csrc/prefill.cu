@@ -409,21 +409,23 @@ __global__ void __launch_bounds__(352, 1)
             for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
                 const Geom G = geom<HM, PK>(item, n_blocks, p, scu, list);
                 if (qc > 0 && !(ok = lane_wait(&bars->q_empty, (qc - 1) & 1, bars))) break;
+                auto load_q = [&](uint64_t *bar) {
+                    mbar_arrive_expect_tx(bar, 2 * C::TILE_BYTES);
+                    for (int hh = 0; hh < 2; ++hh)
+                        for (int bx = 0; bx < C::NBOX; ++bx)
+                            tma_load_3d(sQ + hh * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ, bar,
+                                        bx * 64, G.row0 + G.t0 + hh * 128, G.b * p.Hq + G.hq);
+                };
                 // (the query rows behind the end matter where they become fp16)
-                const bool q_behind = PK && G.n_core_tiles > 0 && G.t0 + 256 > G.T;
-                uint64_t *q_bar = q_behind ? &bars->raw : &bars->q_full;
-                mbar_arrive_expect_tx(q_bar, 2 * C::TILE_BYTES);
-                for (int hh = 0; hh < 2; ++hh)
-                    for (int bx = 0; bx < C::NBOX; ++bx)
-                        tma_load_3d(sQ + hh * C::TILE_BYTES + bx * C::BOX_BYTES, &tmQ,
-                                    q_bar, bx * 64, G.row0 + G.t0 + hh * 128,
-                                    G.b * p.Hq + G.hq);
-                if (q_behind) {
+                if (PK && G.n_core_tiles > 0 && G.t0 + 256 > G.T) {
+                    load_q(&bars->raw);
                     if (!(ok = lane_wait(&bars->raw, raws++ & 1, bars))) break;
                     const int n0 = max(0, G.t0 + 128 - G.T), n1 = min(128, G.t0 + 256 - G.T);
                     mbar_arrive_expect_tx(&bars->q_full, (n0 + n1) * C::NBOX * 128);
                     zero_rows<D>(sQ, n0, &bars->q_full);
                     zero_rows<D>(sQ + C::TILE_BYTES, n1, &bars->q_full);
+                } else {
+                    load_q(&bars->q_full);
                 }
                 ++qc;
                 const int z = G.b * p.Hkv + G.h;
@@ -446,16 +448,20 @@ __global__ void __launch_bounds__(352, 1)
                         const int s = vc % C::VST;
                         if (!(ok = lane_wait(&bars->v_empty[s], ((vc / C::VST) & 1) ^ 1, bars)))
                             break;
-                        const int n_behind = PK ? rows_behind(G, j) : 0;
-                        uint64_t *v_bar = n_behind > 0 ? &bars->raw : &bars->v_full[s];
-                        mbar_arrive_expect_tx(v_bar, C::TILE_BYTES);
-                        for (int bx = 0; bx < C::NBOX; ++bx)
-                            tma_load_3d(sV + s * C::TILE_BYTES + bx * C::BOX_BYTES, mv,
-                                        v_bar, bx * 64, key0, z);
-                        if (n_behind > 0) {
+                        auto load_v = [&](uint64_t *bar) {
+                            mbar_arrive_expect_tx(bar, C::TILE_BYTES);
+                            for (int bx = 0; bx < C::NBOX; ++bx)
+                                tma_load_3d(sV + s * C::TILE_BYTES + bx * C::BOX_BYTES, mv, bar,
+                                            bx * 64, key0, z);
+                        };
+                        if (PK && rows_behind(G, j) > 0) {
+                            load_v(&bars->raw);
                             if (!(ok = lane_wait(&bars->raw, raws++ & 1, bars))) break;
-                            mbar_arrive_expect_tx(&bars->v_full[s], n_behind * C::NBOX * 128);
-                            zero_rows<D>(sV + s * C::TILE_BYTES, n_behind, &bars->v_full[s]);
+                            const int n = rows_behind(G, j);
+                            mbar_arrive_expect_tx(&bars->v_full[s], n * C::NBOX * 128);
+                            zero_rows<D>(sV + s * C::TILE_BYTES, n, &bars->v_full[s]);
+                        } else {
+                            load_v(&bars->v_full[s]);
                         }
                         ++vc;
                     }
