@@ -501,7 +501,9 @@ cca_status cca_paged_fill(const cca_paged_cache *c, int layer, const cca_rows *K
  * Attention of the newest token t = lens[b] - 1 of every row over one
  * layer of the cache: q_t [B, Hq, d] (bf16) -> o_t [B, Hq, d] (o_dtype).
  * A free row gets a zero output; so does a row longer than its table, which
- * is reported (CCA_ERR_CAPACITY).  Keys whose page is missing are left out
+ * is reported (CCA_ERR_CAPACITY).  The same call on the same cache gives the
+ * same bits; how a row's keys are shared out among the SMs depends on the
+ * whole batch, so in another batch its output may differ by roundings.  Keys whose page is missing are left out
  * and reported (CCA_ERR_PAGE).
  */
 cca_status cca_attn_decode_paged(const cca_paged_cache *c, int layer, const void *q_t, void *o_t,
@@ -534,6 +536,9 @@ cca_status cca_paged_step(const cca_paged_cache *c, int layer, const void *q_t, 
  * (rows in order, pages freed by this call included).  A row for
  * whose copies no page is left is freed and reported (CCA_ERR_CAPACITY).  A
  * parent out of range keeps its row and is reported (CCA_ERR_PAGE).
+ * Called between steps: the tokens that rows hold have been written, and
+ * those of the next step are reserved afterwards (a page that a reserved
+ * token fills up would be shared, and not be written).
  */
 cca_status cca_paged_fork(const cca_paged_cache *c, const int32_t *parent, void *workspace,
                           size_t workspace_bytes, cudaStream_t stream);

@@ -907,7 +907,7 @@ def cca_paged_fork(cache: PagedCache, parent, workspace=None, stream=None) -> No
     """Row b becomes what row parent[b] was (int32, CUDA, [B]; b: keeps it,
     -1: frees it), for all layers.  Full pages are shared, partly filled last
     ones copied: samples of one prompt, beams that change places, rows that
-    are done."""
+    are done.  Called between steps, before the next cca_paged_reserve."""
     torch, dev = _torch(), _device(cache.tables, "cache")
     _check(lib().cca_paged_fork(
         cache.struct, _tensor(parent, "parent", (cache.B,), torch.int32, dev),

@@ -465,6 +465,18 @@ def test_two_attentions_at_once(cca):
     assert cca.cca_device_status() == cca.CCA_OK
 
 
+def test_same_call_same_bits(cca):
+    """Over and over, whatever the order in which CTAs arrive at a pair."""
+    import torch
+    r = Rows(cca, 4, 4, 1, 128, 16, 1024, 16, 9000)
+    r.prompts([0, 1, 2, 3], [8800, 1, 5000, 300])
+    q = to_cuda(synth.random_bf16((4, 4, 128), 71))
+    want = cca.cca_attn_decode_paged(r.c, q, out_dtype=torch.float32)
+    for _ in range(50):
+        assert torch.equal(want, cca.cca_attn_decode_paged(r.c, q, out_dtype=torch.float32))
+    assert cca.cca_device_status() == cca.CCA_OK
+
+
 # ---------------------------------------------------------------- refusals on the device
 
 def test_fill_leaves_out_what_does_not_fit(cca):
