@@ -25,6 +25,12 @@ Entry points (same names as the C ABI):
     cca_selftest_wait_timeout, cca_device_status
 and the ``Cache`` and ``PagedCache`` classes holding a decode cache's device
 buffers.
+
+Every call runs on ``stream`` (None: the current one).  What it allocates
+(outputs, a workspace) belongs to that stream, as with PyTorch calls made
+under ``torch.cuda.stream(stream)``: before another stream uses an output it
+waits for that stream, and ``record_stream`` tells PyTorch of a use that may
+outlast the tensor.
 """
 
 from __future__ import annotations
@@ -209,6 +215,26 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on(stream):
+    """Context in which ``stream`` is the current one."""
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
+def _new(like, shape, dtype, stream, fill=None):
+    """A tensor on the device of ``like`` for a call on ``stream`` (None: the
+    current one), from that stream's pool: memory of another stream's pool
+    could still be in use by work queued there, and would go back to it while
+    the call's own work has yet to run."""
+    if stream is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t if fill is None else t.fill_(fill)
+    with _on(stream):
+        return _new(like, shape, dtype, None, fill)
+
+
 def _dev(t, name: str, dtype=None):
     """Pointer of a contiguous CUDA tensor (None passes NULL)."""
     if t is None:
@@ -243,9 +269,9 @@ def cca_pool(Q, K, V, g: int, Kc=None, Vc=None, stream=None):
     Hkv = K.shape[1]
     m = T // g
     if Kc is None:
-        Kc = torch.empty((B, Hkv, m, d), dtype=torch.float16, device=Q.device)
+        Kc = _new(Q, (B, Hkv, m, d), torch.float16, stream)
     if Vc is None:
-        Vc = torch.empty((B, Hkv, m, d), dtype=torch.float16, device=Q.device)
+        Vc = _new(Q, (B, Hkv, m, d), torch.float16, stream)
     if tuple(K.shape) != (B, Hkv, T, d) or tuple(V.shape) != (B, Hkv, T, d):
         raise ValueError("K and V must be [B, Hkv, T, d]")
     if tuple(Kc.shape) != (B, Hkv, m, d) or tuple(Vc.shape) != (B, Hkv, m, d):
@@ -269,7 +295,7 @@ def cca_attn_prefill(Q, K, V, Kc, Vc, g: int, w: int, O=None,
     Hkv = K.shape[1]
     if O is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
-        O = torch.empty((B, Hq, T, d), dtype=dt, device=Q.device)
+        O = _new(Q, (B, Hq, T, d), dt, stream)
     od = _odtype(O.dtype)
     if tuple(O.shape) != (B, Hq, T, d):
         raise ValueError("O must be [B, Hq, T, d]")
@@ -289,9 +315,9 @@ def cca_attn_prefill_lse(Q, K, V, Kc, Vc, g: int, w: int, O=None, out_dtype=None
     Hkv = K.shape[1]
     if O is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
-        O = torch.empty((B, Hq, T, d), dtype=dt, device=Q.device)
+        O = _new(Q, (B, Hq, T, d), dt, stream)
     if lse is None:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=Q.device)
+        lse = _new(Q, (B, Hq, T), torch.float32, stream)
     od = _odtype(O.dtype)
     if tuple(O.shape) != (B, Hq, T, d) or tuple(lse.shape) != (B, Hq, T):
         raise ValueError("O must be [B, Hq, T, d] and lse [B, Hq, T]")
@@ -316,13 +342,12 @@ def cca_attn_backward(Q, K, V, Kc, Vc, O, lse, dO, g: int, w: int, dQ=None, dK=N
     torch = _torch()
     B, Hq, T, d = Q.shape
     Hkv = K.shape[1]
-    f32 = dict(dtype=torch.float32, device=Q.device)
-    dQ = torch.empty((B, Hq, T, d), **f32) if dQ is None else dQ
-    dK = torch.empty((B, Hkv, T, d), **f32) if dK is None else dK
-    dV = torch.empty((B, Hkv, T, d), **f32) if dV is None else dV
+    dQ = _new(Q, (B, Hq, T, d), torch.float32, stream) if dQ is None else dQ
+    dK = _new(Q, (B, Hkv, T, d), torch.float32, stream) if dK is None else dK
+    dV = _new(Q, (B, Hkv, T, d), torch.float32, stream) if dV is None else dV
     nbytes = cca_attn_backward_workspace_bytes(B, Hq, Hkv, T, d, g)
     if workspace is None:
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=Q.device)
+        workspace = _new(Q, max(nbytes, 256), torch.uint8, stream)
     _check(lib().cca_attn_backward(
         _dev(Q, "Q"), _dev(K, "K"), _dev(V, "V"), _dev(Kc, "Kc", torch.float16),
         _dev(Vc, "Vc", torch.float16), _dev(O, "O", O.dtype), _odtype(O.dtype),
@@ -434,9 +459,9 @@ def cca_lca_pool(Q, K, V, g: int, d_rope: int, Kc=None, Vc=None, stream=None):
     Hkv = K.shape[1]
     m = T // g
     if Kc is None:
-        Kc = torch.empty((B, Hkv, m, d), dtype=torch.float16, device=Q.device)
+        Kc = _new(Q, (B, Hkv, m, d), torch.float16, stream)
     if Vc is None:
-        Vc = torch.empty((B, Hkv, m, d), dtype=torch.float16, device=Q.device)
+        Vc = _new(Q, (B, Hkv, m, d), torch.float16, stream)
     if tuple(K.shape) != (B, Hkv, T, d) or tuple(V.shape) != (B, Hkv, T, d):
         raise ValueError("K and V must be [B, Hkv, T, d]")
     if tuple(Kc.shape) != (B, Hkv, m, d) or tuple(Vc.shape) != (B, Hkv, m, d):
@@ -487,10 +512,10 @@ def cca_attn_decode(cache: Cache, q_t, o_t=None, out_dtype=None,
     torch = _torch()
     if o_t is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
-        o_t = torch.empty(tuple(q_t.shape), dtype=dt, device=q_t.device)
+        o_t = _new(q_t, tuple(q_t.shape), dt, stream)
     od = _odtype(o_t.dtype)
     if workspace is None:
-        workspace = _cache_workspace(cache, q_t.device)
+        workspace = _cache_workspace(cache, q_t, stream)
     _check(lib().cca_attn_decode(
         ctypes.byref(cache.struct), _dev(q_t, "q_t"), _dev(o_t, "o_t", o_t.dtype),
         od, ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
@@ -498,13 +523,12 @@ def cca_attn_decode(cache: Cache, q_t, o_t=None, out_dtype=None,
     return o_t
 
 
-def _cache_workspace(cache: Cache, device):
+def _cache_workspace(cache: Cache, like, stream):
     """The cache's own decode workspace, zero-filled when (re)allocated, as
-    cca_decode_step requires before its first use."""
-    torch = _torch()
+    cca_decode_step requires before its first use, on the call's stream."""
     nbytes = cca_decode_workspace_bytes(cache)
     if cache.workspace is None or cache.workspace.numel() < nbytes:
-        cache.workspace = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        cache.workspace = _new(like, max(nbytes, 256), _torch().uint8, stream, fill=0)
     return cache.workspace
 
 
@@ -517,10 +541,10 @@ def cca_decode_step(cache: Cache, q_t, k_t, v_t, o_t=None, out_dtype=None,
     torch = _torch()
     if o_t is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
-        o_t = torch.empty(tuple(q_t.shape), dtype=dt, device=q_t.device)
+        o_t = _new(q_t, tuple(q_t.shape), dt, stream)
     od = _odtype(o_t.dtype)
     if workspace is None:
-        workspace = _cache_workspace(cache, q_t.device)
+        workspace = _cache_workspace(cache, q_t, stream)
     _check(lib().cca_decode_step(
         ctypes.byref(cache.struct), _dev(q_t, "q_t"), _dev(k_t, "k_t"), _dev(v_t, "v_t"),
         _dev(o_t, "o_t", o_t.dtype), od, ctypes.c_void_p(workspace.data_ptr()),
@@ -555,10 +579,10 @@ def cca_attn_decode_rows(cache: Cache, lens, q_t, o_t=None, out_dtype=None,
         raise ValueError("lens needs one entry per batch row")
     if o_t is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
-        o_t = torch.empty(tuple(q_t.shape), dtype=dt, device=q_t.device)
+        o_t = _new(q_t, tuple(q_t.shape), dt, stream)
     od = _odtype(o_t.dtype)
     if workspace is None:
-        workspace = _cache_workspace(cache, q_t.device)
+        workspace = _cache_workspace(cache, q_t, stream)
     _check(lib().cca_attn_decode_rows(
         ctypes.byref(cache.struct), _lens(lens), _dev(q_t, "q_t"),
         _dev(o_t, "o_t", o_t.dtype), od, ctypes.c_void_p(workspace.data_ptr()),
@@ -572,7 +596,7 @@ def cca_attn_decode_noalloc(cache: Cache, q_t, o_t=None, out_dtype=None, stream=
     torch = _torch()
     if o_t is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
-        o_t = torch.empty(tuple(q_t.shape), dtype=dt, device=q_t.device)
+        o_t = _new(q_t, tuple(q_t.shape), dt, stream)
     od = _odtype(o_t.dtype)
     _check(lib().cca_attn_decode_noalloc(
         ctypes.byref(cache.struct), _dev(q_t, "q_t"), _dev(o_t, "o_t", o_t.dtype), od,
@@ -654,7 +678,7 @@ def cca_pool_packed(Q, K, V, cu, g: int, Kc=None, Vc=None, stream=None):
     Hq, Hkv, total, d = _packed_shapes(Q, K)
     shape = (Hkv, total // int(g) if g > 0 else 0, d)
     if Kc is None and Vc is None:
-        Kc, Vc = Q.new_empty((2, *shape), dtype=torch.float16).unbind(0)
+        Kc, Vc = _new(Q, (2, *shape), torch.float16, stream).unbind(0)
     elif Kc is None or Vc is None:
         raise ValueError("give both Kc and Vc, or neither")
     _check(lib().cca_pool_packed(
@@ -684,22 +708,18 @@ def cca_attn_prefill_packed(Q, K, V, Kc, Vc, cu, g: int, w: int, O=None, out_dty
     S = cu.shape[0] - 1
     if O is None:
         dt = torch.bfloat16 if out_dtype is None else out_dtype
-        if Q.is_contiguous():
-            O = Q.new_empty((Hq, total, d), dtype=dt)
-        elif Q.stride(0) < Q.stride(1):  # [total, Hq, d] in memory
-            O = Q.new_empty((total, Hq, d), dtype=dt).transpose(0, 1)
+        if not Q.is_contiguous() and Q.stride(0) < Q.stride(1):  # [total, Hq, d] in memory
+            O = _new(Q, (total, Hq, d), dt, stream).transpose(0, 1)
         else:
-            O = Q.new_empty((Hq, total, d), dtype=dt)
+            O = _new(Q, (Hq, total, d), dt, stream)
     ws, nbytes = None, 0
     if workspace is not None:
         ws, nbytes = _here(workspace, "workspace", dev), workspace.numel()
     elif S > 0:
         nbytes = lib().cca_packed_workspace_bytes(S, total)
         if nbytes:
-            workspace = Q.new_empty(nbytes, dtype=torch.uint8)
+            workspace = _new(Q, nbytes, torch.uint8, stream)
             ws = workspace.data_ptr()
-            if stream is not None:  # freed on return: not before that stream's work is done
-                workspace.record_stream(stream)
     core = (Hkv, total // int(g) if g > 0 else 0, d)
     _check(lib().cca_attn_prefill_packed(
         _rows(Q, "Q", (Hq, total, d), bf, dev), _rows(K, "K", (Hkv, total, d), bf, dev),
@@ -876,7 +896,7 @@ def cca_attn_decode_paged(cache: PagedCache, q_t, layer: int = 0, o_t=None, out_
     torch, dev = _torch(), _device(cache.tables, "cache")
     shape = cache.q_shape
     if o_t is None:
-        o_t = q_t.new_empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
+        o_t = _new(q_t, shape, torch.bfloat16 if out_dtype is None else out_dtype, stream)
     _check(lib().cca_attn_decode_paged(
         cache.struct, int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16, dev),
         _tensor(o_t, "o_t", shape, o_t.dtype, dev), _odtype(o_t.dtype),
@@ -894,7 +914,7 @@ def cca_paged_step(cache: PagedCache, q_t, k_t, v_t, layer: int = 0, o_t=None, o
     torch, dev = _torch(), _device(cache.tables, "cache")
     shape, kv = cache.q_shape, cache.kv_shape
     if o_t is None:
-        o_t = q_t.new_empty(shape, dtype=torch.bfloat16 if out_dtype is None else out_dtype)
+        o_t = _new(q_t, shape, torch.bfloat16 if out_dtype is None else out_dtype, stream)
     _check(lib().cca_paged_step(
         cache.struct, int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16, dev),
         _tensor(k_t, "k_t", kv, torch.bfloat16, dev), _tensor(v_t, "v_t", kv, torch.bfloat16, dev),
@@ -920,7 +940,7 @@ def cca_paged_compact(cache: PagedCache, live=None, workspace=None, stream=None)
     raw pool."""
     torch, dev = _torch(), _device(cache.tables, "cache")
     if live is None:
-        live = cache.tables.new_empty(2, dtype=torch.int64)
+        live = _new(cache.tables, 2, torch.int64, stream)
     _check(lib().cca_paged_compact(
         cache.struct, _tensor(live, "live", (2,), torch.int64, dev),
         *_paged_workspace(cache, workspace, dev), _raw_stream(stream, dev)), "cca_paged_compact")
