@@ -250,6 +250,17 @@ def _dev(t, name: str, dtype=None):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _workspace(t):
+    """Address and bytes of a caller's workspace: contiguous, so that as many
+    bytes as it has elements lie behind its address (an expanded tensor has
+    less memory than that)."""
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if not t.is_cuda:
+        raise ValueError("workspace must be a CUDA tensor")
+    return ctypes.c_void_p(t.data_ptr()), t.numel() * t.element_size()
+
+
 def _odtype(out_dtype) -> int:
     torch = _torch()
     if out_dtype in (torch.bfloat16, "bf16"):
@@ -353,7 +364,7 @@ def cca_attn_backward(Q, K, V, Kc, Vc, O, lse, dO, g: int, w: int, dQ=None, dK=N
         _dev(Vc, "Vc", torch.float16), _dev(O, "O", O.dtype), _odtype(O.dtype),
         _dev(lse, "lse", torch.float32), _dev(dO, "dO"), _dev(dQ, "dQ", torch.float32),
         _dev(dK, "dK", torch.float32), _dev(dV, "dV", torch.float32), B, Hq, Hkv, T, d, int(g),
-        int(w), ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream(stream)),
+        int(w), *_workspace(workspace), _stream(stream)),
         "cca_attn_backward")
     return dQ, dK, dV
 
@@ -518,8 +529,7 @@ def cca_attn_decode(cache: Cache, q_t, o_t=None, out_dtype=None,
         workspace = _cache_workspace(cache, q_t, stream)
     _check(lib().cca_attn_decode(
         ctypes.byref(cache.struct), _dev(q_t, "q_t"), _dev(o_t, "o_t", o_t.dtype),
-        od, ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-        _stream(stream)), "cca_attn_decode")
+        od, *_workspace(workspace), _stream(stream)), "cca_attn_decode")
     return o_t
 
 
@@ -547,8 +557,8 @@ def cca_decode_step(cache: Cache, q_t, k_t, v_t, o_t=None, out_dtype=None,
         workspace = _cache_workspace(cache, q_t, stream)
     _check(lib().cca_decode_step(
         ctypes.byref(cache.struct), _dev(q_t, "q_t"), _dev(k_t, "k_t"), _dev(v_t, "v_t"),
-        _dev(o_t, "o_t", o_t.dtype), od, ctypes.c_void_p(workspace.data_ptr()),
-        workspace.numel(), _stream(stream)), "cca_decode_step")
+        _dev(o_t, "o_t", o_t.dtype), od, *_workspace(workspace), _stream(stream)),
+        "cca_decode_step")
     return o_t
 
 
@@ -585,8 +595,8 @@ def cca_attn_decode_rows(cache: Cache, lens, q_t, o_t=None, out_dtype=None,
         workspace = _cache_workspace(cache, q_t, stream)
     _check(lib().cca_attn_decode_rows(
         ctypes.byref(cache.struct), _lens(lens), _dev(q_t, "q_t"),
-        _dev(o_t, "o_t", o_t.dtype), od, ctypes.c_void_p(workspace.data_ptr()),
-        workspace.numel(), _stream(stream)), "cca_attn_decode_rows")
+        _dev(o_t, "o_t", o_t.dtype), od, *_workspace(workspace), _stream(stream)),
+        "cca_attn_decode_rows")
     return o_t
 
 
@@ -714,7 +724,8 @@ def cca_attn_prefill_packed(Q, K, V, Kc, Vc, cu, g: int, w: int, O=None, out_dty
             O = _new(Q, (Hq, total, d), dt, stream)
     ws, nbytes = None, 0
     if workspace is not None:
-        ws, nbytes = _here(workspace, "workspace", dev), workspace.numel()
+        _here(workspace, "workspace", dev)
+        ws, nbytes = _workspace(workspace)
     elif S > 0:
         nbytes = lib().cca_packed_workspace_bytes(S, total)
         if nbytes:
@@ -852,7 +863,8 @@ def cca_paged_workspace_bytes(cache: PagedCache) -> int:
 def _paged_workspace(cache: PagedCache, workspace, dev: int):
     if workspace is None:  # (on the cache's device)
         return cache.workspace_at
-    return _here(workspace, "workspace", dev), workspace.numel()
+    _here(workspace, "workspace", dev)
+    return _workspace(workspace)
 
 
 def cca_paged_reserve(cache: PagedCache, n, stream=None) -> None:

@@ -57,6 +57,7 @@ def allocations(monkeypatch):
     monkeypatch.setattr(cca, "lib", _Lib)
     monkeypatch.setattr(cca, "_dev", point)
     monkeypatch.setattr(cca, "_lens", point)
+    monkeypatch.setattr(cca, "_workspace", lambda t: (point(t), t.numel()))
     monkeypatch.setattr(cca, "_here", lambda t, name, dev: t.data_ptr())
     monkeypatch.setattr(cca, "_device", lambda t, name: 0)
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda at, **kw: at)
