@@ -261,6 +261,15 @@ def _workspace(t):
     return ctypes.c_void_p(t.data_ptr()), t.numel() * t.element_size()
 
 
+def _int(x, name: str, bits: int = 32) -> int:
+    """A number for a C integer of so many bits, to which ctypes would cut it
+    without a word."""
+    x = int(x)
+    if x >> (bits - 1) not in (0, -1):
+        raise ValueError(f"{name} = {x} does not fit in {bits} bits")
+    return x
+
+
 def _odtype(out_dtype) -> int:
     torch = _torch()
     if out_dtype in (torch.bfloat16, "bf16"):
@@ -290,7 +299,7 @@ def cca_pool(Q, K, V, g: int, Kc=None, Vc=None, stream=None):
     _check(lib().cca_pool(_dev(Q, "Q"), _dev(K, "K"), _dev(V, "V"),
                           _dev(Kc, "Kc", torch.float16), _dev(Vc, "Vc", torch.float16),
                           B, Hq, Hkv, T, d,
-                          int(g), _stream(stream)), "cca_pool")
+                          _int(g, "g"), _stream(stream)), "cca_pool")
     return Kc, Vc
 
 
@@ -312,8 +321,8 @@ def cca_attn_prefill(Q, K, V, Kc, Vc, g: int, w: int, O=None,
         raise ValueError("O must be [B, Hq, T, d]")
     _check(lib().cca_attn_prefill(
         _dev(Q, "Q"), _dev(K, "K"), _dev(V, "V"), _dev(Kc, "Kc", torch.float16),
-        _dev(Vc, "Vc", torch.float16), _dev(O, "O", O.dtype), od, B, Hq, Hkv, T, d, int(g),
-        int(w), _stream(stream)), "cca_attn_prefill")
+        _dev(Vc, "Vc", torch.float16), _dev(O, "O", O.dtype), od, B, Hq, Hkv, T, d, _int(g, "g"),
+        _int(w, "w"), _stream(stream)), "cca_attn_prefill")
     return O
 
 
@@ -335,14 +344,14 @@ def cca_attn_prefill_lse(Q, K, V, Kc, Vc, g: int, w: int, O=None, out_dtype=None
     _check(lib().cca_attn_prefill_lse(
         _dev(Q, "Q"), _dev(K, "K"), _dev(V, "V"), _dev(Kc, "Kc", torch.float16),
         _dev(Vc, "Vc", torch.float16), _dev(O, "O", O.dtype), od,
-        _dev(lse, "lse", torch.float32), B, Hq, Hkv, T, d, int(g), int(w), _stream(stream)),
-        "cca_attn_prefill_lse")
+        _dev(lse, "lse", torch.float32), B, Hq, Hkv, T, d, _int(g, "g"), _int(w, "w"),
+        _stream(stream)), "cca_attn_prefill_lse")
     return O, lse
 
 
 def cca_attn_backward_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, d: int, g: int) -> int:
     return int(lib().cca_attn_backward_workspace_bytes(int(B), int(Hq), int(Hkv), int(T),
-                                                       int(d), int(g)))
+                                                       int(d), _int(g, "g")))
 
 
 def cca_attn_backward(Q, K, V, Kc, Vc, O, lse, dO, g: int, w: int, dQ=None, dK=None,
@@ -363,8 +372,8 @@ def cca_attn_backward(Q, K, V, Kc, Vc, O, lse, dO, g: int, w: int, dQ=None, dK=N
         _dev(Q, "Q"), _dev(K, "K"), _dev(V, "V"), _dev(Kc, "Kc", torch.float16),
         _dev(Vc, "Vc", torch.float16), _dev(O, "O", O.dtype), _odtype(O.dtype),
         _dev(lse, "lse", torch.float32), _dev(dO, "dO"), _dev(dQ, "dQ", torch.float32),
-        _dev(dK, "dK", torch.float32), _dev(dV, "dV", torch.float32), B, Hq, Hkv, T, d, int(g),
-        int(w), *_workspace(workspace), _stream(stream)),
+        _dev(dK, "dK", torch.float32), _dev(dV, "dV", torch.float32), B, Hq, Hkv, T, d,
+        _int(g, "g"), _int(w, "w"), *_workspace(workspace), _stream(stream)),
         "cca_attn_backward")
     return dQ, dK, dV
 
@@ -385,7 +394,8 @@ class Cache:
         self.v_tail = torch.zeros((B, Hkv, tail_cap, d), **kw)
         self.struct = _CacheStruct(self.k_core.data_ptr(), self.v_core.data_ptr(),
                                    self.k_tail.data_ptr(), self.v_tail.data_ptr(),
-                                   B, Hq, Hkv, d, g, w, core_cap, tail_cap, 0)
+                                   *(_int(x, "a size of Cache") for x in (B, Hq, Hkv, d, g, w)),
+                                   core_cap, tail_cap, 0)
         self.workspace = None
 
     def row(self, b: int) -> "Cache":
@@ -479,8 +489,8 @@ def cca_lca_pool(Q, K, V, g: int, d_rope: int, Kc=None, Vc=None, stream=None):
         raise ValueError("Kc and Vc must be [B, Hkv, T // g, d]")
     _check(lib().cca_lca_pool(_dev(Q, "Q"), _dev(K, "K"), _dev(V, "V"),
                               _dev(Kc, "Kc", torch.float16), _dev(Vc, "Vc", torch.float16),
-                              B, Hq, Hkv, T, d, int(g), int(d_rope), _stream(stream)),
-           "cca_lca_pool")
+                              B, Hq, Hkv, T, d, _int(g, "g"), _int(d_rope, "d_rope"),
+                              _stream(stream)), "cca_lca_pool")
     return Kc, Vc
 
 
@@ -503,14 +513,16 @@ def cca_lca_cache_prefill(cache: Cache, q_sum, Q, K, V, d_rope: int, stream=None
     T = Q.shape[2]
     _check(lib().cca_lca_cache_prefill(ctypes.byref(cache.struct), _qsum(cache, q_sum),
                                        _dev(Q, "Q"), _dev(K, "K"), _dev(V, "V"), T,
-                                       int(d_rope), _stream(stream)), "cca_lca_cache_prefill")
+                                       _int(d_rope, "d_rope"), _stream(stream)),
+           "cca_lca_cache_prefill")
 
 
 def cca_lca_cache_append(cache: Cache, q_sum, q_t, k_t, v_t, d_rope: int, stream=None) -> None:
     """Append one token with LCA condensation of the group it completes."""
     _check(lib().cca_lca_cache_append(ctypes.byref(cache.struct), _qsum(cache, q_sum),
                                       _dev(q_t, "q_t"), _dev(k_t, "k_t"), _dev(v_t, "v_t"),
-                                      int(d_rope), _stream(stream)), "cca_lca_cache_append")
+                                      _int(d_rope, "d_rope"), _stream(stream)),
+           "cca_lca_cache_append")
 
 
 def cca_decode_workspace_bytes(cache: Cache) -> int:
@@ -695,7 +707,7 @@ def cca_pool_packed(Q, K, V, cu, g: int, Kc=None, Vc=None, stream=None):
         _rows(Q, "Q", (Hq, total, d), bf, dev), _rows(K, "K", (Hkv, total, d), bf, dev),
         _rows(V, "V", (Hkv, total, d), bf, dev), _offsets(cu, dev),
         _tensor(Kc, "Kc", shape, torch.float16, dev), _tensor(Vc, "Vc", shape, torch.float16, dev),
-        cu.shape[0] - 1, Hq, Hkv, total, d, int(g),
+        cu.shape[0] - 1, Hq, Hkv, total, d, _int(g, "g"),
         _raw_stream(stream, dev)), "cca_pool_packed")
     return Kc, Vc
 
@@ -737,8 +749,8 @@ def cca_attn_prefill_packed(Q, K, V, Kc, Vc, cu, g: int, w: int, O=None, out_dty
         _rows(V, "V", (Hkv, total, d), bf, dev),
         None if Kc is None else _tensor(Kc, "Kc", core, torch.float16, dev),
         None if Vc is None else _tensor(Vc, "Vc", core, torch.float16, dev), _offsets(cu, dev),
-        _rows(O, "O", (Hq, total, d), O.dtype, dev), _odtype(O.dtype), S, Hq, Hkv, total, d, int(g),
-        int(w), ws, nbytes, _raw_stream(stream, dev)), "cca_attn_prefill_packed")
+        _rows(O, "O", (Hq, total, d), O.dtype, dev), _odtype(O.dtype), S, Hq, Hkv, total, d,
+        _int(g, "g"), _int(w, "w"), ws, nbytes, _raw_stream(stream, dev)), "cca_attn_prefill_packed")
     return O
 
 
@@ -792,8 +804,8 @@ class PagedCache:
         self.struct = _PagedStruct(
             *(t.data_ptr() for t in (*pools, self.core_table, self.raw_table, self.core_ref,
                                      self.raw_ref, self.lens)),
-            layers, B, int(Hq), Hkv, d, int(g), int(w), page, core_cols, raw_cols, core_pages,
-            raw_pages)
+            layers, B, _int(Hq, "Hq"), Hkv, d, _int(g, "g"), _int(w, "w"), page, core_cols,
+            raw_cols, core_pages, raw_pages)
         # zero-filled once, as the library asks for
         self.workspace = torch.zeros(max(cca_paged_workspace_bytes(self), 256),
                                      dtype=torch.uint8, device=device)
@@ -876,8 +888,8 @@ def cca_paged_reserve(cache: PagedCache, n, stream=None) -> None:
         each, n = _tensor(n, "n", (cache.B,), torch.int64, dev), 0
     else:
         each = None
-    _check(lib().cca_paged_reserve(cache.struct, each, int(n), _raw_stream(stream, dev)),
-           "cca_paged_reserve")
+    _check(lib().cca_paged_reserve(cache.struct, each, _int(n, "n", 64),
+                                   _raw_stream(stream, dev)), "cca_paged_reserve")
 
 
 def cca_paged_fill(cache: PagedCache, K, V, Kc, Vc, cu, rows, layer: int = 0,
@@ -891,7 +903,7 @@ def cca_paged_fill(cache: PagedCache, K, V, Kc, Vc, cu, rows, layer: int = 0,
     S = cu.shape[0] - 1
     shape, core = (cache.Hkv, total, cache.d), (cache.Hkv, total // cache.g, cache.d)
     _check(lib().cca_paged_fill(
-        cache.struct, int(layer), _rows(K, "K", shape, torch.bfloat16, dev),
+        cache.struct, _int(layer, "layer"), _rows(K, "K", shape, torch.bfloat16, dev),
         _rows(V, "V", shape, torch.bfloat16, dev),
         None if Kc is None else _tensor(Kc, "Kc", core, torch.float16, dev),
         None if Vc is None else _tensor(Vc, "Vc", core, torch.float16, dev), _offsets(cu, dev),
@@ -910,7 +922,7 @@ def cca_attn_decode_paged(cache: PagedCache, q_t, layer: int = 0, o_t=None, out_
     if o_t is None:
         o_t = _new(q_t, shape, torch.bfloat16 if out_dtype is None else out_dtype, stream)
     _check(lib().cca_attn_decode_paged(
-        cache.struct, int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16, dev),
+        cache.struct, _int(layer, "layer"), _tensor(q_t, "q_t", shape, torch.bfloat16, dev),
         _tensor(o_t, "o_t", shape, o_t.dtype, dev), _odtype(o_t.dtype),
         *_paged_workspace(cache, workspace, dev), _raw_stream(stream, dev)),
         "cca_attn_decode_paged")
@@ -928,7 +940,7 @@ def cca_paged_step(cache: PagedCache, q_t, k_t, v_t, layer: int = 0, o_t=None, o
     if o_t is None:
         o_t = _new(q_t, shape, torch.bfloat16 if out_dtype is None else out_dtype, stream)
     _check(lib().cca_paged_step(
-        cache.struct, int(layer), _tensor(q_t, "q_t", shape, torch.bfloat16, dev),
+        cache.struct, _int(layer, "layer"), _tensor(q_t, "q_t", shape, torch.bfloat16, dev),
         _tensor(k_t, "k_t", kv, torch.bfloat16, dev), _tensor(v_t, "v_t", kv, torch.bfloat16, dev),
         _tensor(o_t, "o_t", shape, o_t.dtype, dev), _odtype(o_t.dtype),
         *_paged_workspace(cache, workspace, dev), _raw_stream(stream, dev)), "cca_paged_step")

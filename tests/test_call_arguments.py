@@ -110,3 +110,44 @@ class _Ws:
 def test_workspace_size_is_in_bytes():
     at, n = cca._workspace(_Ws())
     assert (at.value, n) == (4096, 256)
+
+
+BIG = 1 << 32  # what ctypes would pass as 0
+
+
+def _numbers():
+    q, k, core = _bf(4, 96, 64), _bf(2, 96, 64), torch.zeros((2, 6, 64), dtype=F16)
+    cu, rows = torch.tensor([0, 96], dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    qt, kt = _bf(3, 4, 64), _bf(3, 2, 64)
+    q4, k4, c4 = q[None], k[None], core[None]
+    return {
+        "window of prompts": lambda x: cca.cca_attn_prefill_packed(q, k, k, core, core, cu, 16, x),
+        "window of a paged cache": lambda x: _paged(w=x),
+        "heads of a paged cache": lambda x: _paged(Hq=x),
+        "layer of a fill": lambda x: cca.cca_paged_fill(_paged(), k, k, core, core, cu, rows,
+                                                        layer=x),
+        "layer of a step": lambda x: cca.cca_paged_step(_paged(), qt, kt, kt, layer=x),
+        "layer of an attention": lambda x: cca.cca_attn_decode_paged(_paged(), qt, layer=x),
+        "tokens": lambda x: cca.cca_paged_reserve(_paged(), x << 32),
+        "window of a prompt": lambda x: cca.cca_attn_prefill(q4, k4, k4, c4, c4, 16, x),
+        "window of a cache": lambda x: cca.Cache(3, 4, 2, 64, 16, x, 8, tail_cap=80, device="cpu"),
+    }
+
+
+@pytest.mark.parametrize("name", ["window of prompts", "window of a paged cache",
+                                  "heads of a paged cache", "layer of a fill", "layer of a step",
+                                  "layer of an attention", "tokens", "window of a prompt",
+                                  "window of a cache"])
+def test_numbers_beyond_the_librarys_are_refused(lib, monkeypatch, name):
+    monkeypatch.setattr(cca, "_workspace", lambda t: (0, t.numel()))
+    with pytest.raises(ValueError, match="does not fit"):
+        _numbers()[name](BIG)
+    assert not [c for c in lib.calls if not c[0].endswith("bytes")]
+
+
+def test_int():
+    assert [cca._int(x, "x") for x in (0, -1, 2**31 - 1, -2**31)] == [0, -1, 2**31 - 1, -2**31]
+    assert cca._int(2**40, "x", 64) == 2**40
+    for x in (2**31, -2**31 - 1, 1 << 80):
+        with pytest.raises(ValueError):
+            cca._int(x, "x")
