@@ -750,7 +750,8 @@ def cca_attn_prefill_packed(Q, K, V, Kc, Vc, cu, g: int, w: int, O=None, out_dty
         None if Kc is None else _tensor(Kc, "Kc", core, torch.float16, dev),
         None if Vc is None else _tensor(Vc, "Vc", core, torch.float16, dev), _offsets(cu, dev),
         _rows(O, "O", (Hq, total, d), O.dtype, dev), _odtype(O.dtype), S, Hq, Hkv, total, d,
-        _int(g, "g"), _int(w, "w"), ws, nbytes, _raw_stream(stream, dev)), "cca_attn_prefill_packed")
+        _int(g, "g"), _int(w, "w"), ws, nbytes, _raw_stream(stream, dev)),
+        "cca_attn_prefill_packed")
     return O
 
 

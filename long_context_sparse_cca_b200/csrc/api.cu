@@ -483,7 +483,7 @@ cca_status cca_pool_packed(const cca_rows *Q, const cca_rows *K, const cca_rows 
 {
     const cca_status s = packed_status(S, Hq, Hkv, total, d, g, 0, cu);
     if (s != CCA_OK) return s;
-    if (cca::pool_packed_smem(S, Hq / Hkv, g) > 227u * 1024u) return CCA_ERR_UNSUPPORTED;
+    if (cca::pool_packed_smem(S, Hq / Hkv, g) > cca::kSmemMost) return CCA_ERR_UNSUPPORTED;
     const int64_t m = total / g;
     if (m == 0) return CCA_OK;
     cca::PackedRows q, k, v;

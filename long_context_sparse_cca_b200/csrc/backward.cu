@@ -1279,10 +1279,7 @@ cudaError_t launch_bw(const void *Q, const void *K, const void *V, const void *K
         const int64_t groups = static_cast<int64_t>(B) * Hkv * m;
         const int64_t want = (groups + warps - 1) / warps;
         const int blocks = static_cast<int>(want < 148LL * 16 ? want : 148LL * 16);
-        if (smem > 48 * 1024 &&
-            (e = cudaFuncSetAttribute(bw_pool_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(smem))) != cudaSuccess)
-            return e;
+        if ((e = allow_smem(bw_pool_kernel<D>, smem)) != cudaSuccess) return e;
         bw_pool_kernel<D><<<blocks, warps * 32, smem, s>>>(
             static_cast<const uint16_t *>(Q), static_cast<const uint16_t *>(K),
             static_cast<const uint16_t *>(V), p);

@@ -159,9 +159,7 @@ cudaError_t launch_append(const void *q_t, const void *k_t, const void *v_t,
     const size_t smem = sizeof(float) * kAppendWarps * (r * g + g);
     const float scale_log2 = kLog2e / sqrtf(static_cast<float>(d));
     auto args = [&](auto kern) {
-        if (smem > 48 * 1024)
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
+        allow_smem(kern, smem);
         kern<<<blocks, kAppendWarps * 32, smem, s>>>(
             static_cast<const uint16_t *>(q_t), static_cast<const uint16_t *>(k_t),
             static_cast<const uint16_t *>(v_t), static_cast<uint16_t *>(k_core),
@@ -185,9 +183,7 @@ cudaError_t launch_append_rows(const void *q_t, const void *k_t, const void *v_t
     const size_t smem = sizeof(float) * Hkv * (r * g + g);
     const float scale_log2 = kLog2e / sqrtf(static_cast<float>(d));
     auto args = [&](auto kern) {
-        if (smem > 48 * 1024)
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
+        allow_smem(kern, smem, 16);  // (a row's length)
         kern<<<B, Hkv * 32, smem, s>>>(
             static_cast<const uint16_t *>(q_t), static_cast<const uint16_t *>(k_t),
             static_cast<const uint16_t *>(v_t), static_cast<uint16_t *>(k_core),

@@ -529,9 +529,7 @@ cudaError_t launch_split(const CacheView &cv, const void *q_t, float *part_o,
     const int lg_floats = STEP ? std::max(R * kDecodeChunk, (r + 1) * st.g) : R * kDecodeChunk;
     const size_t smem = sizeof(float) * (lg_floats + S::NG * R * D + 2 * R);
     auto kern = decode_split_kernel<D, R, STEP>;
-    if (smem > 48 * 1024)
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
+    allow_smem(kern, smem, 16);  // (whether this CTA is the last one)
     dim3 grid(nsplit, B * Hkv);
     kern<<<grid, kDecodeThreads, smem, s>>>(cv, st, static_cast<const uint16_t *>(q_t),
                                             part_o, part_ml, tickets, o_t, o_f32 ? 1 : 0,

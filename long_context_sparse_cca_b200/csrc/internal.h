@@ -66,6 +66,21 @@ cudaError_t launch_prefill(const void *Q, const void *K, const void *V,
                            int B, int Hq, int Hkv, int64_t T, int d, int g,
                            int w, cudaStream_t s, float *lse = nullptr);
 
+// Shared memory that a block may have.
+constexpr size_t kSmemMost = 227 * 1024;
+
+// Before a launch with smem bytes of dynamic shared memory: allows the kernel
+// all that its `own` static bytes leave, not only what this call asks for.
+// The allowance is the process's, and another host thread's call may set it
+// between this and the launch.
+template <class K>
+cudaError_t allow_smem(K kern, size_t smem, size_t own = 0)
+{
+    if (smem <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(kSmemMost - own));
+}
+
 // Launch a kernel that begins with chain_begin() (common.cuh): its blocks
 // may be set up while the kernel before it in the stream still runs.
 template <class... P, class... A>

@@ -458,9 +458,7 @@ cudaError_t launch_lca_pool(const void *Q, const void *K, const void *V, void *K
     auto *kc = static_cast<uint16_t *>(Kc);
     auto *vc = static_cast<uint16_t *>(Vc);
     auto go = [&](auto kern) {
-        if (smem > 48 * 1024)
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
+        allow_smem(kern, smem);
         kern<<<blocks, kLcaWarps * 32, smem, s>>>(q, k, v, kc, vc, Hq, Hkv, T, g, d_rope, m,
                                                    out_rows, n_groups, scale_log2);
     };
@@ -493,9 +491,7 @@ cudaError_t launch_lca_append(const void *q_t, const void *k_t, const void *v_t,
     const size_t smem = sizeof(float) * kLcaAppendWarps * (r * g + g);
     const float scale_log2 = kLog2e / sqrtf(static_cast<float>(d));
     auto go = [&](auto kern) {
-        if (smem > 48 * 1024)
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
+        allow_smem(kern, smem);
         kern<<<blocks, kLcaAppendWarps * 32, smem, s>>>(
             static_cast<const uint16_t *>(q_t), static_cast<const uint16_t *>(k_t),
             static_cast<const uint16_t *>(v_t), q_sum, static_cast<uint16_t *>(k_core),

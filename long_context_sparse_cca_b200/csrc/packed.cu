@@ -159,10 +159,7 @@ cudaError_t launch_pool_packed(const PackedRows &Q, const PackedRows &K, const P
     const float scale_log2 = kLog2e / sqrtf(static_cast<float>(d));
     cudaError_t e = cudaSuccess;
     auto go = [&](auto kern) {
-        if (smem > 48 * 1024)
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem));
-        if (e != cudaSuccess) return;
+        if ((e = allow_smem(kern, smem)) != cudaSuccess) return;
         e = launch_chained(kern, blocks, kPoolWarps * 32, smem, s, Q, K, V, cu,
                            static_cast<uint16_t *>(Kc), static_cast<uint16_t *>(Vc), S, Hkv, r,
                            total, g, m, scale_log2);

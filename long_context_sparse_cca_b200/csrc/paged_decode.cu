@@ -53,6 +53,7 @@ namespace {
 
 constexpr int kPart = 16;  // rows of a part of a tile, which lie in one page
 constexpr int kCtas = 148;  // one per SM
+constexpr size_t kOwnSmem = 1100;  // at least the kernel's static shared memory
 
 template <int D>
 struct Pd {
@@ -1033,8 +1034,7 @@ cudaError_t launch_paged_decode(const cca_paged_cache &c, int layer, const void 
     const float scale_log2 = kLog2e / sqrtf(static_cast<float>(c.d));
     auto go = [&](auto kern, int warps, int stages) {
         const size_t smem = decode_smem(c.d, r, warps, stages, c.B);
-        const cudaError_t e = cudaFuncSetAttribute(
-            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        const cudaError_t e = allow_smem(kern, smem, kOwnSmem);
         if (e != cudaSuccess) return e;
         return launch_chained(kern, kCtas, warps * 32, smem, s, v, static_cast<const uint16_t *>(q_t),
                               static_cast<const uint16_t *>(k_t),
@@ -1049,8 +1049,8 @@ cudaError_t launch_paged_decode(const cca_paged_cache &c, int layer, const void 
         return k_t != nullptr ? go(paged_decode_kernel<D, W, S, WIDE, true>, W, S)
                               : go(paged_decode_kernel<D, W, S, WIDE, false>, W, S);
     };
-    auto fits = [&](int warps, int stages) {  // in 227 KB, about 1 KB of them the kernel's own
-        return decode_smem(c.d, r, warps, stages, c.B) <= 227u * 1024u - 1100u;
+    auto fits = [&](int warps, int stages) {
+        return decode_smem(c.d, r, warps, stages, c.B) <= kSmemMost - kOwnSmem;
     };
     using std::integral_constant;
     const integral_constant<int, 128> d128{};

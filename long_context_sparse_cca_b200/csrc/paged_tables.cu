@@ -717,10 +717,7 @@ cudaError_t launch_paged_fill(const cca_paged_cache &c, int layer, const PackedR
     const size_t smem = sizeof(int) * (S + 1 + c.B);
     cudaError_t e = cudaSuccess;
     auto go = [&](auto kern) {
-        if (smem > 48 * 1024)
-            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(smem));
-        if (e != cudaSuccess) return;
+        if ((e = allow_smem(kern, smem)) != cudaSuccess) return;
         e = launch_chained(kern, grid, 256, smem, s, v, K, V, static_cast<const uint16_t *>(Kc),
                            static_cast<const uint16_t *>(Vc), cu, rows, S, total, m);
     };

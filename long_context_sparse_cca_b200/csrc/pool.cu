@@ -74,9 +74,7 @@ cudaError_t launch_pool(const void *Q, const void *K, const void *V, void *Kc,
     auto *kc = static_cast<uint16_t *>(Kc);
     auto *vc = static_cast<uint16_t *>(Vc);
     auto go = [&](auto kern) {
-        if (smem > 48 * 1024)
-            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
+        allow_smem(kern, smem);
         kern<<<blocks, kPoolWarps * 32, smem, s>>>(q, k, v, kc, vc, Hq, Hkv, T, g, m,
                                                     out_rows, n_groups, scale_log2);
     };
