@@ -483,6 +483,19 @@ cca_status cca_paged_reserve(const cca_paged_cache *c, const long long *n_new, l
                              cudaStream_t stream);
 
 /*
+ * cca_paged_reserve for a loop of steps: also notes in the workspace which
+ * rows it refused.  Such a row is held: cca_paged_step with the same
+ * workspace leaves it as it is (zero output, nothing written), so that its
+ * last token is not written over, until a later call gives it room.  A row
+ * that is given nothing because it asked for nothing stays what it was.
+ * cca_paged_fork with this workspace hands the note on with the row.  A
+ * workspace that holds notes serves one cache only, until it is zero-filled
+ * again.
+ */
+cca_status cca_paged_reserve_held(const cca_paged_cache *c, const long long *n_new, long long n,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Fill one layer's pages from packed prompts: sequence s becomes row
  * rows[s] (int32, device memory) of the cache, which cca_paged_reserve has
  * given the length of the sequence.  K, V: packed bf16 tensors [Hkv]; Kc,
@@ -516,8 +529,10 @@ cca_status cca_attn_decode_paged(const cca_paged_cache *c, int layer, const void
  * cca_paged_reserve has made room) to its page, pools the group it completes
  * into its core row, and computes cca_attn_decode_paged of it.  lens is not
  * changed, so that the layers of a model take their steps one after the
- * other.  (A row that cca_paged_reserve refused still ends in the token
- * before: its step writes that one again.)  A token or core row whose page
+ * other.  A row that cca_paged_reserve_held refused is left as it is and gets
+ * a zero output.  (After cca_paged_reserve, which leaves no note, a row
+ * without new room still ends in the token before, and its step writes that
+ * one again.)  A token or core row whose page
  * is missing or belongs to another row as well is not written, and is
  * reported (CCA_ERR_PAGE).
  */

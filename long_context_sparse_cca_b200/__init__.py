@@ -19,8 +19,8 @@ Entry points (same names as the C ABI):
     LCA variant's condensation; ``lca_query_sums`` allocates the running
     query sums its cache calls keep), cca_pool_packed,
     cca_packed_workspace_bytes, cca_attn_prefill_packed (prompts of different
-    lengths without padding), cca_paged_workspace_bytes, cca_paged_reserve,
-    cca_paged_fill, cca_attn_decode_paged, cca_paged_step, cca_paged_fork,
+    lengths without padding), cca_paged_workspace_bytes, cca_paged_reserve
+    (cca_paged_reserve_held of the C ABI), cca_paged_fill, cca_attn_decode_paged, cca_paged_step, cca_paged_fork,
     cca_paged_compact (a decode cache whose rows share memory in pages),
     cca_selftest_wait_timeout, cca_device_status
 and the ``Cache`` and ``PagedCache`` classes holding a decode cache's device
@@ -65,7 +65,8 @@ EXPORTS = ("cca_pool", "cca_attn_prefill", "cca_cache_prefill",
            "cca_attn_prefill_lse", "cca_attn_backward", "cca_attn_backward_workspace_bytes",
            "cca_lca_pool", "cca_lca_cache_prefill", "cca_lca_cache_append",
            "cca_pool_packed", "cca_packed_workspace_bytes", "cca_attn_prefill_packed",
-           "cca_paged_workspace_bytes", "cca_paged_reserve", "cca_paged_fill",
+           "cca_paged_workspace_bytes", "cca_paged_reserve", "cca_paged_reserve_held",
+           "cca_paged_fill",
            "cca_attn_decode_paged", "cca_paged_step", "cca_paged_fork", "cca_paged_compact")
 
 
@@ -159,6 +160,8 @@ def lib():
     L.cca_paged_workspace_bytes.restype = sz
     L.cca_paged_reserve.argtypes = [PP, P, ctypes.c_longlong, P]
     L.cca_paged_reserve.restype = st
+    L.cca_paged_reserve_held.argtypes = [PP, P, ctypes.c_longlong, P, sz, P]
+    L.cca_paged_reserve_held.restype = st
     L.cca_paged_fill.argtypes = [PP, i, RP, RP, P, P, P, P, i, i64, P]
     L.cca_paged_fill.restype = st
     L.cca_attn_decode_paged.argtypes = [PP, i, P, P, i, P, sz, P]
@@ -880,17 +883,21 @@ def _paged_workspace(cache: PagedCache, workspace, dev: int):
     return _workspace(workspace)
 
 
-def cca_paged_reserve(cache: PagedCache, n, stream=None) -> None:
+def cca_paged_reserve(cache: PagedCache, n, stream=None, workspace=None) -> None:
     """Lengthen rows and give them the pages of their new tokens: ``n`` is a
     number of tokens for every row that is not free, or an int64 CUDA tensor
-    [B] of each row's.  Raw pages before the new window are given back."""
+    [B] of each row's.  Raw pages before the new window are given back.  A row
+    that does not fit keeps its length and pages (CCA_ERR_CAPACITY of
+    cca_device_status), and cca_paged_step with the same workspace leaves it
+    as it is until a later call gives it room."""
     torch, dev = _torch(), _device(cache.tables, "cache")
     if isinstance(n, torch.Tensor):
         each, n = _tensor(n, "n", (cache.B,), torch.int64, dev), 0
     else:
         each = None
-    _check(lib().cca_paged_reserve(cache.struct, each, _int(n, "n", 64),
-                                   _raw_stream(stream, dev)), "cca_paged_reserve")
+    _check(lib().cca_paged_reserve_held(cache.struct, each, _int(n, "n", 64),
+                                        *_paged_workspace(cache, workspace, dev),
+                                        _raw_stream(stream, dev)), "cca_paged_reserve")
 
 
 def cca_paged_fill(cache: PagedCache, K, V, Kc, Vc, cu, rows, layer: int = 0,
@@ -935,7 +942,8 @@ def cca_paged_step(cache: PagedCache, q_t, k_t, v_t, layer: int = 0, o_t=None, o
     """One decode step of one layer in one launch: append the newest token of
     every row (q_t [B,Hq,d], k_t/v_t [B,Hkv,d]; cca_paged_reserve(cache, 1)
     has made room for it, once for all layers) and return its attention
-    output o_t [B,Hq,d].  Capturable in a CUDA graph."""
+    output o_t [B,Hq,d].  A row that cca_paged_reserve refused stays as it is
+    and gets zeros.  Capturable in a CUDA graph."""
     torch, dev = _torch(), _device(cache.tables, "cache")
     shape, kv = cache.q_shape, cache.kv_shape
     if o_t is None:

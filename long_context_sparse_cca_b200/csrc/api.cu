@@ -558,7 +558,18 @@ cca_status cca_paged_reserve(const cca_paged_cache *c, const long long *n_new, l
     const cca_status s = paged_status(c);
     if (s != CCA_OK) return s;
     if (n_new != nullptr ? !aligned_to(n_new, 8) : n < 0) return CCA_ERR_INVALID_ARG;
-    return from_cuda(cca::launch_paged_reserve(*c, n_new, n, stream));
+    return from_cuda(cca::launch_paged_reserve(*c, n_new, n, nullptr, stream));
+}
+
+cca_status cca_paged_reserve_held(const cca_paged_cache *c, const long long *n_new, long long n,
+                                  void *workspace, size_t workspace_bytes, cudaStream_t stream)
+{
+    const cca_status s = paged_status(c);
+    if (s != CCA_OK) return s;
+    if ((n_new != nullptr ? !aligned_to(n_new, 8) : n < 0) ||
+        !paged_workspace_ok(*c, workspace, workspace_bytes))
+        return CCA_ERR_INVALID_ARG;
+    return from_cuda(cca::launch_paged_reserve(*c, n_new, n, workspace, stream));
 }
 
 cca_status cca_paged_fill(const cca_paged_cache *c, int layer, const cca_rows *K,

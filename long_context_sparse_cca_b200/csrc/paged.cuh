@@ -12,6 +12,7 @@ struct PagedView {
     uint16_t *k_core, *v_core, *k_raw, *v_raw;  // the layer's pools
     const int *core_table, *raw_table, *core_ref, *raw_ref;
     const long long *lens;
+    const long long *held;  // [B] (cca_paged_step): a row of this many tokens is held
     int B, Hq, Hkv, g, w;
     int shift;  // log2(page)
     int core_cols, raw_cols, core_pages, raw_pages;
@@ -77,7 +78,7 @@ inline PagedView paged_view(const cca_paged_cache &c, int layer)
     const int64_t core = layer * page * c.core_pages, raw = layer * page * c.raw_pages;
     return {static_cast<uint16_t *>(c.k_core) + core, static_cast<uint16_t *>(c.v_core) + core,
             static_cast<uint16_t *>(c.k_raw) + raw, static_cast<uint16_t *>(c.v_raw) + raw,
-            c.core_table, c.raw_table, c.core_ref, c.raw_ref, c.lens, c.B, c.Hq, c.Hkv, c.g, c.w,
+            c.core_table, c.raw_table, c.core_ref, c.raw_ref, c.lens, nullptr, c.B, c.Hq, c.Hkv, c.g, c.w,
             __builtin_ctz(c.page), c.core_cols, c.raw_cols, c.core_pages, c.raw_pages,
             paged_max_len(c.raw_cols, c.core_cols, c.g, __builtin_ctz(c.page))};
 }

@@ -11,7 +11,8 @@ namespace cca {
 // Workspace of a paged cache (byte offsets, 256-byte aligned).
 struct PagedWorkspace {
     size_t tickets, part;                          // decode: arrivals, partial results
-    size_t lens, flags, core_tmp, raw_tmp;         // fork: old lengths, new tables
+    size_t held;                                   // lengths at which rows were refused room
+    size_t lens, old_held, flags, core_tmp, raw_tmp;  // fork: as they were, new tables
     size_t lists, counts;                          // fork, compact: page moves
     size_t total;
 };
@@ -25,7 +26,7 @@ cudaError_t launch_paged_fill(const cca_paged_cache &c, int layer, const PackedR
                               const PackedRows &V, const void *Kc, const void *Vc, const int *cu,
                               const int *rows, int S, int64_t total, cudaStream_t s);
 cudaError_t launch_paged_reserve(const cca_paged_cache &c, const long long *n_new, long long n,
-                                 cudaStream_t s);
+                                 void *workspace, cudaStream_t s);  // workspace: NULL: no marks
 cudaError_t launch_paged_fork(const cca_paged_cache &c, const int *parent, void *workspace,
                               cudaStream_t s);
 cudaError_t launch_paged_compact(const cca_paged_cache &c, long long *live, void *workspace,

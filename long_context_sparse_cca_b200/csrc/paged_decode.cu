@@ -128,13 +128,16 @@ struct RowTiles {
     int core, all;
 };
 
-template <int KEYS>
+template <int KEYS, bool STEP>
 __device__ __forceinline__ RowTiles row_tiles(const PagedView &c, int b, bool &over)
 {
     RowTiles r;
     const int64_t len = __ldg(c.lens + b);
+    // a step takes a row that was refused room for its token as free: it would
+    // write the token over the row's last one
+    const bool held = STEP && __ldg(c.held + b) == len;
     over = len > c.longest;  // a row longer than its table is taken as free
-    r.len = over || len < 0 ? 0 : len;
+    r.len = over || held || len < 0 ? 0 : len;
     // groups before the window of token t: max(t - w, 0) / g, in 32 bits where
     // they do (a 64-bit division takes a hundred instructions)
     const int64_t past = r.len - 1 - c.w;
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
         for (int b = b0; b < b1; ++b) {
             bool over;
             before[b] = n;
-            const int all = row_tiles<P::KEYS>(c, b, over).all;
+            const int all = row_tiles<P::KEYS, STEP>(c, b, over).all;
             n += (static_cast<int64_t>(all) << 13) + (all > 0);
             if (over && blockIdx.x == 0) atomicOr(&g_paged_decode_status, kStatusCapacity);
         }
@@ -621,7 +624,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 
     if (n_tiles > 0) {
         bool over, bad = false;
-        RowTiles row = row_tiles<P::KEYS>(c, at_b, over);
+        RowTiles row = row_tiles<P::KEYS, STEP>(c, at_b, over);
         int from = 0, id = 0;  // pages of the parts PARTS * from + lane of the pair
         auto load_ids = [&]() {
             from = at_i;
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                 at_h = 0;
                 do {
                     if (++at_b >= c.B) return;  // the end of the list
-                    row = row_tiles<P::KEYS>(c, at_b, over);
+                    row = row_tiles<P::KEYS, STEP>(c, at_b, over);
                 } while (row.all == 0);
             }
             load_ids();
@@ -1030,7 +1033,8 @@ cudaError_t launch_paged_decode(const cca_paged_cache &c, int layer, const void 
     const PagedWorkspace w = paged_workspace(c);
     char *base = static_cast<char *>(workspace);
     const int r = c.Hq / c.Hkv;
-    const PagedView v = paged_view(c, layer);
+    PagedView v = paged_view(c, layer);
+    v.held = reinterpret_cast<const long long *>(base + w.held);
     const float scale_log2 = kLog2e / sqrtf(static_cast<float>(c.d));
     auto go = [&](auto kern, int warps, int stages) {
         const size_t smem = decode_smem(c.d, r, warps, stages, c.B);

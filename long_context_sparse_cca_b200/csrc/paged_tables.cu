@@ -110,7 +110,8 @@ struct Grow {
 };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
-    reserve_kernel(TablesView v, const long long *__restrict__ n_new, long long n_all)
+    reserve_kernel(TablesView v, const long long *__restrict__ n_new, long long n_all,
+                   long long *__restrict__ held)
 {
     // of each row: wanted pages of my pool before it, [B], and the column of
     // its first one (-1: nothing granted), [B]
@@ -171,7 +172,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
         // (no page is taken for what lies beyond the last free one)
         before[b] = static_cast<int>(min(at[me], static_cast<int64_t>(INT32_MAX)));
         column[b] = ok && r.n > 0 ? (me == 0 ? r.core : r.raw) : -1;
-        if (me == 0 && (!ok || r.refused)) report(kStatusCapacity);
+        if (me == 0 && (!ok || r.refused)) {
+            report(kStatusCapacity);
+            if (held != nullptr) held[b] = r.len;
+        }
         at[0] += r.n_core;
         at[1] += r.n_raw;
     }
@@ -220,6 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads)
             if (column[b] >= 0) {
                 const Grow r = row_of(b);
                 v.lens[b] = r.len + r.n;
+                if (held != nullptr) held[b] = 0;
             }
 }
 
@@ -324,7 +329,8 @@ struct ForkView {
     TablesView v;
     const int *parent;
     int *tmp[2];          // new tables
-    long long *old_lens;  // [B]
+    long long *held;      // [B] of the workspace: goes with the row
+    long long *old_lens, *old_held;  // [B]
     int *flags;           // [B]: bit p: a copy in pool p; kFlagRow
     int2 *list[2];        // copies (from, to); to = -1: none
     int *counts;          // [2] copies, [2] live
@@ -358,6 +364,7 @@ __device__ __forceinline__ void fork_row(const ForkView &f, int b, int me, int n
     const int p = parent_of(f, b);
     if (me == 0) {
         f.old_lens[b] = v.lens[b];
+        f.old_held[b] = f.held[b];
         if (p != f.parent[b]) report(kStatusPage);
     }
     if (p == b) {
@@ -548,7 +555,10 @@ __global__ void __launch_bounds__(256)
                 for (int c = tlo + threadIdx.x; c < thi; c += blockDim.x)
                     if (tmp[c] >= 0) atomicSub(pool.ref + tmp[c], 1);
         }
-        if (threadIdx.x == 0) v.lens[b] = len;
+        if (threadIdx.x == 0) {
+            v.lens[b] = len;
+            f.held[b] = none ? 0 : f.old_held[p];
+        }
     }
     copy_pages(f.list[0], f.counts[0], layers, core);
     copy_pages(f.list[1], f.counts[1], layers, raw);
@@ -684,7 +694,9 @@ PagedWorkspace paged_workspace(const cca_paged_cache &c)
     };
     w.tickets = part(sizeof(unsigned int) * c.B * c.Hkv);
     w.part = part(paged_decode_part_bytes(c));
+    w.held = part(sizeof(long long) * c.B);
     w.lens = part(sizeof(long long) * c.B);
+    w.old_held = part(sizeof(long long) * c.B);
     w.flags = part(sizeof(int) * c.B);
     w.core_tmp = part(sizeof(int) * static_cast<size_t>(c.B) * c.core_cols);
     w.raw_tmp = part(sizeof(int) * static_cast<size_t>(c.B) * c.raw_cols);
@@ -697,10 +709,14 @@ PagedWorkspace paged_workspace(const cca_paged_cache &c)
 }
 
 cudaError_t launch_paged_reserve(const cca_paged_cache &c, const long long *n_new, long long n,
-                                 cudaStream_t s)
+                                 void *workspace, cudaStream_t s)
 {
+    long long *held = nullptr;
+    if (workspace != nullptr)
+        held = reinterpret_cast<long long *>(static_cast<char *>(workspace) +
+                                             paged_workspace(c).held);
     return launch_chained(reserve_kernel, 2, kThreads, sizeof(int) * 2 * c.B, s, tables_view(c),
-                          n_new, n);
+                          n_new, n, held);
 }
 
 cudaError_t launch_paged_fill(const cca_paged_cache &c, int layer, const PackedRows &K,
@@ -738,7 +754,9 @@ cudaError_t launch_paged_fork(const cca_paged_cache &c, const int *parent, void 
     f.parent = parent;
     f.tmp[0] = reinterpret_cast<int *>(base + w.core_tmp);
     f.tmp[1] = reinterpret_cast<int *>(base + w.raw_tmp);
+    f.held = reinterpret_cast<long long *>(base + w.held);
     f.old_lens = reinterpret_cast<long long *>(base + w.lens);
+    f.old_held = reinterpret_cast<long long *>(base + w.old_held);
     f.flags = reinterpret_cast<int *>(base + w.flags);
     f.list[0] = reinterpret_cast<int2 *>(base + w.lists);
     f.list[1] = f.list[0] + c.B;
