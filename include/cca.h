@@ -474,7 +474,12 @@ size_t cca_paged_workspace_bytes(const cca_paged_cache *c);
  * for its complete groups.  The free pages of lowest number are taken, rows
  * in order, a row's columns in order; then the raw pages that lie wholly
  * before the new window are given back.  The new tokens' contents are
- * written by cca_paged_fill or cca_paged_step.  A row that does not fit (its
+ * written by cca_paged_fill (the whole sequence) or cca_paged_step (the newest
+ * token).  So a row that holds tokens and is given more than one, a further
+ * prompt for instance, has to be filled again from its first token before
+ * anything reads it: its pages' new rows hold anything until then, and no
+ * call can tell.  (For that all its pages have to be its own, as after a
+ * prompt and its steps.)  A row that does not fit (its
  * table's columns; or the pages that it and the rows before it need exceed
  * the free ones of a pool) keeps its length and pages and is reported by
  * cca_device_status (CCA_ERR_CAPACITY).

@@ -887,7 +887,8 @@ def cca_paged_reserve(cache: PagedCache, n, stream=None, workspace=None) -> None
     """Lengthen rows and give them the pages of their new tokens: ``n`` is a
     number of tokens for every row that is not free, or an int64 CUDA tensor
     [B] of each row's.  Raw pages before the new window are given back.  A row
-    that does not fit keeps its length and pages (CCA_ERR_CAPACITY of
+    that held tokens and is given more than one has to be filled again as a
+    whole (cca_paged_fill) before anything reads it.  A row that does not fit keeps its length and pages (CCA_ERR_CAPACITY of
     cca_device_status), and cca_paged_step with the same workspace leaves it
     as it is until a later call gives it room."""
     torch, dev = _torch(), _device(cache.tables, "cache")

@@ -184,6 +184,40 @@ def test_held_row_is_handed_on_and_freed(built):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("more", [2, 16, 75])
+def test_further_prompt_fills_the_whole_row_again(built, more):
+    """A row given several tokens at once is the whole sequence, filled again;
+    the tokens between are not left as the pages' former rows had them."""
+    import torch
+    r = Loop(2, [50, 33], 12, 30, layers=1)
+    for t in r.c.pools[2:]:  # what free pages and rows without a token hold
+        t[:, r.c.raw_ref == 0] = float("nan")
+    for _ in range(3):
+        r.step()
+    cca.cca_paged_reserve(r.c, torch.tensor([more, 0], device="cuda"))
+    assert cca.cca_device_status() == cca.CCA_OK
+    new = packed_inputs([more], HQ, HKV, D, 77)[:3]
+    h = r.hist[0][0] = [np.concatenate([x, y], 1) for x, y in zip(r.hist[0][0], new)]
+    n = h[0].shape[1]
+    assert r.c.lens.tolist() == [n, 36]
+    Q, K, V = (to_cuda(x) for x in h)
+    cu, row = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [0]))
+    # not the new tokens alone: they are not as long as the row
+    cca.cca_paged_fill(r.c, K[:, :more], V[:, :more],
+                       *cca.cca_pool_packed(Q[:, :more], K[:, :more], V[:, :more],
+                                            cu - torch.tensor([0, n - more], device="cuda").int(), G),
+                       cu - torch.tensor([0, n - more], device="cuda").int(), row)
+    assert cca.cca_device_status() == cca.CCA_ERR_PAGE
+    cca.cca_paged_fill(r.c, K, V, *cca.cca_pool_packed(Q, K, V, cu, G), cu, row)
+    assert cca.cca_device_status() == cca.CCA_OK
+    q = Q[:, -1].expand(2, HQ, D).contiguous()
+    o = cca.cca_attn_decode_paged(r.c, q, out_dtype=torch.float32)
+    r.check(0, 0, o[0], h)
+    for _ in range(2):
+        r.step()
+
+
+@pytest.mark.gpu
 def test_rows_that_ask_for_nothing_stay_what_they_were(built):
     """n = 0 neither holds a row nor lets it go."""
     import torch
