@@ -28,9 +28,12 @@
 // one type: for core tiles the query row is rounded to fp16 after a power of
 // two brought its largest entry to 2^13 .. 2^14 (exact but for entries below
 // 2^-27 of that one).  P is split into two numbers of the tile's type, P =
-// P_hi + P_lo up to 2^-17, so that P V is as good as with fp32 weights; for
-// up to 8 query heads P_lo takes the fragment rows that are free, and costs
-// nothing.  Scores, running maximum and sum, and outputs are fp32.
+// P_hi + P_lo up to 2^-17; for up to 8 query heads P_lo takes the fragment
+// rows that are free, and costs nothing.  fp16 has no numbers below 2^-24, so
+// core tiles hold weights relative to 2^-15 of the largest one (up to 2^15
+// then): one of 2^-n of the largest is off by 2^-17 of itself down to n = 23,
+// and by 2^-40 of the largest below.  Scores, running maximum and sum, and
+// outputs are fp32.
 //
 // Stretches that share a pair are joined in shared memory within a CTA, and
 // across CTAs by the last one that arrives at the pair (a ticket), always in
@@ -179,6 +182,9 @@ __device__ __forceinline__ void put8(void *o_t, int o_f32, int64_t at, const flo
 // last, kPage << i: part i has a page.
 constexpr int kCore = 1 << 12, kNewest = 1 << 13, kFirst = 1 << 14, kEnds = 1 << 15,
               kPage = 1 << 16;
+
+// Weights of core tiles are 2^(score - maximum + kCoreUp).
+constexpr float kCoreUp = 15.f;
 
 // What a pair costs a warp beside its tiles (queries, output, page numbers),
 // and what a pooling does, in tiles: by the timeline of a batch of 64 rows of
@@ -742,7 +748,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                     }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const float to = fmaxf(m[x], top);
+                const float to = fmaxf(m[x], F16 ? top - kCoreUp : top);
                 const float use = to == -INFINITY ? 0.f : to;
                 if (__any_sync(0xffffffffu, to > m[x])) {
                     const float f = fast_exp2(m[x] - use);
@@ -821,6 +827,20 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
             const int flags = mt.z;
             const bool core = flags & kCore;
             if (flags & kFirst) from_start = true;
+            if (loaded && q_core != core) {
+                // from the pair's core rows to its raw ones, whose weights are
+                // relative to the maximum itself
+                const float f = fast_exp2(-kCoreUp);
+#pragma unroll
+                for (int y = 0; y < QR; ++y) {
+                    m[y] += kCoreUp;
+                    l[y] *= f;
+                }
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[n][e] *= f;
+            }
             if (!loaded || q_core != core) {
                 load_q(mt.x, mt.y, core);
                 loaded = true;
