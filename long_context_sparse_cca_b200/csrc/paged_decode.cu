@@ -28,8 +28,10 @@
 // one type: for core tiles the query row is rounded to fp16 after a power of
 // two brought its largest entry to 2^13 .. 2^14 (exact but for entries below
 // 2^-27 of that one).  P is split into two numbers of the tile's type, P =
-// P_hi + P_lo up to 2^-17; for up to 8 query heads P_lo takes the fragment
-// rows that are free, and costs nothing.  fp16 has no numbers below 2^-24, so
+// P_hi + P_lo up to 2^-17 (raw rows of more than 8 query heads: 2^-16, see
+// split2); for up to 8 query heads P_lo takes the fragment rows that are free,
+// and costs nothing.  An infinite value gives an infinite output, as with one
+// number, and not NaN.  fp16 has no numbers below 2^-24, so
 // core tiles hold weights relative to 2^-15 of the largest one (up to 2^15
 // then): one of 2^-n of the largest is off by 2^-17 of itself down to n = 23,
 // and by 2^-40 of the largest below.  Scores, running maximum and sum, and
@@ -98,12 +100,19 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // (x0, x1) as a pair of the tile's type and the pair of what that leaves.
-template <bool F16>
+// ABOVE (bf16, x >= 0): what is left is above zero wherever x is, for sums
+// that both numbers go into: with a value of infinity, zero would make them
+// NaN, and less than zero too.  So the first number is cut off and not
+// rounded (both together: off by 2^-16), and 2^-20 of x is added to the other.
+template <bool F16, bool ABOVE>
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t &hi, uint32_t &lo)
 {
     if constexpr (F16) {
         hi = pack_f16x2(x0, x1);
         lo = pack_f16x2(x0 - f16_lo(hi), x1 - f16_hi(hi));
+    } else if constexpr (ABOVE) {
+        hi = __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632);
+        lo = pack_bf16x2(fmaf(x0, 0x1p-20f, x0 - bf16_lo(hi)), fmaf(x1, 0x1p-20f, x1 - bf16_hi(hi)));
     } else {
         hi = pack_bf16x2(x0, x1);
         lo = pack_bf16x2(x0 - bf16_lo(hi), x1 - bf16_hi(hi));
@@ -769,7 +778,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                     const float p0 = fast_exp2(s[n][2 * x] - use);
                     const float p1 = fast_exp2(s[n][2 * x + 1] - use);
                     l[x] += p0 + p1;
-                    split2<F16>(p0, p1, ph[x][n], pl[x][n]);
+                    split2<F16, WIDE>(p0, p1, ph[x][n], pl[x][n]);
                 }
             }
 #pragma unroll
@@ -875,7 +884,11 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 #pragma unroll
                             for (int n = 0; n < 8; ++n) {
                                 const float(&a)[4] = o[h * 8 + n];
-                                y8[n] = (WIDE ? a[2 * y + e] : a[e] + a[2 + e]) * inv;
+                                // (an infinite value times P_lo is infinite
+                                // with any sign, or NaN)
+                                const float hi = WIDE ? a[2 * y + e] : a[e];
+                                const bool both = !WIDE && fabsf(hi) < INFINITY;
+                                y8[n] = (both ? hi + a[2 + e] : hi) * inv;
                             }
                             const int dim = h * 64 + (2 * qj + e) * 8;
                             if (whole)

@@ -164,6 +164,60 @@ def test_outputs_within_the_bound(built, case):
         assert _off(o[b], _reference(c, q, b)) <= 1, b
 
 
+def _infinite(c, at):
+    """Values of raw rows: at[i] = (row, token, head, dim, value)."""
+    for b, t, h, dim, x in at:
+        page = int(c.raw_table[b, t // c.page])
+        assert page >= 0
+        c.v_raw[0, page, h, t % c.page, dim] = x
+
+
+INF = float("inf")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 128), (8, 1, 64), (12, 1, 128), (32, 2, 64)])
+@pytest.mark.parametrize("lens,g,w", [([5, 33, 64], 16, 64), ([200, 90], 8, 40),
+                                      ([9000, 7000, 1], 16, 1 << 30), ([20000], 16, 8000)])
+def test_infinite_values(built, Hq, Hkv, d, lens, g, w):
+    """An infinite value makes the outputs that see it infinite, as in the
+    formula; infinities of both signs and NaN make them NaN; all others are
+    what they were.  In one warp's tiles, and in many CTAs'."""
+    c, q = _filled(lens, Hq, Hkv, d, g, w, 64, "cuda", seed=d)
+    last, mid = lens[0] - 1, lens[0] - min(lens[0], w) // 2 - 1
+    _infinite(c, [(0, last, 0, 3, INF), (0, mid, 0, 40, -INF), (0, last, Hkv - 1, d - 1, INF),
+                  (0, mid, Hkv - 1, d - 1, -INF), (0, mid, 0, 17, float("nan")),
+                  (len(lens) - 1, lens[-1] - 1, 0, 0, -INF)])
+    o = cca.cca_attn_decode_paged(c, q, out_dtype=F32)
+    assert cca.cca_device_status() == cca.CCA_OK
+    seen = torch.zeros(3, dtype=torch.int64)
+    for b in range(c.B):
+        ref = _reference(c, q, b)
+        for i, kind in enumerate((torch.isnan, torch.isposinf, torch.isneginf)):
+            assert torch.equal(kind(o[b]), kind(ref[0])), (b, kind)
+            seen[i] += int(kind(ref[0]).sum())
+        fine = torch.isfinite(ref[0])
+        zeros = [torch.where(fine, x, 0.0) for x in (o[b], *ref[:3])]
+        assert _off(zeros[0], (*zeros[1:], *ref[3:])) <= 1, b
+    r = Hq // Hkv
+    assert seen.tolist() == [2 * r, r, 2 * r]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq", [2, 24])
+def test_infinite_value_of_the_newest_token(built, Hq):
+    c, q = _filled([30, 100], Hq, 2, 64, 16, 1 << 30, 16, "cuda")
+    k, v = (torch.zeros((2, 2, 64), dtype=BF, device="cuda") for _ in range(2))
+    v[1, 0, 9], v[0, 1, 50] = INF, -INF
+    o = cca.cca_paged_step(c, q, k, v, out_dtype=F32)
+    assert cca.cca_device_status() == cca.CCA_OK
+    for b in range(2):
+        ref = _reference(c, q, b)[0]
+        assert torch.equal(torch.isinf(o[b]), torch.isinf(ref))
+        assert torch.equal(o[b].sign()[torch.isinf(ref)], ref.float().sign()[torch.isinf(ref)])
+        assert not bool(torch.isnan(o[b]).any())
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("B,Hkv", [(1, 1), (8, 16)])  # a tile for each warp, and many
 def test_light_core_rows_behind_a_heavy_one(built, B, Hkv):
