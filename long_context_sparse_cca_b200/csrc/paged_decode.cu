@@ -639,7 +639,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
 
     if (n_tiles > 0) {
         bool over, bad = false;
-        RowTiles row = row_tiles<P::KEYS, STEP>(c, at_b, over);
+        // (rows that have tiles are not held)
+        RowTiles row = row_tiles<P::KEYS, false>(c, at_b, over);
         int from = 0, id = 0;  // pages of the parts PARTS * from + lane of the pair
         auto load_ids = [&]() {
             from = at_i;
@@ -703,8 +704,8 @@ __global__ void __launch_bounds__(WARPS * 32, 1)
                 at_h = 0;
                 do {
                     if (++at_b >= c.B) return;  // the end of the list
-                    row = row_tiles<P::KEYS, STEP>(c, at_b, over);
-                } while (row.all == 0);
+                } while (before[at_b + 1] == before[at_b]);
+                row = row_tiles<P::KEYS, false>(c, at_b, over);
             }
             load_ids();
         };

@@ -75,3 +75,42 @@ def test_rounds_backwards(built, lens, Hq, Hkv, d, g, w):
     assert 2 * sms <= items and items % sms != 0
     assert (sum(lens) // 256 + len(lens)) * Hq <= 8 * sms
     _check(lens, Hq, Hkv, d, g, w, every=1 if len(lens) < 20 else 9)
+
+
+def test_list_in_a_workspace_of_the_callers(built):
+    """More than 64 sequences, in a captured graph with a workspace of the
+    caller's: each replay makes the list anew, from the offsets it finds."""
+    S, d, g, w = 70, 64, 8, 40
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    total = 9000
+    Q, K, V = (torch.randn((h, total, d), generator=gen, device="cuda").to(torch.bfloat16)
+               for h in (4, 2, 2))
+    cu = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    n = cca.cca_packed_workspace_bytes(S, total)
+    assert n > 0
+    ws = torch.full((n,), 0xff, dtype=torch.uint8, device="cuda")
+    core = [torch.zeros((2, total // g, d), dtype=torch.float16, device="cuda") for _ in range(2)]
+    O = torch.zeros_like(Q)
+
+    def run(**kw):
+        cca.cca_pool_packed(Q, K, V, cu, g, *core)
+        return cca.cca_attn_prefill_packed(Q, K, V, *core, cu, g, w, **kw)
+    run(O=O, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(O=O, workspace=ws)
+    for seed in range(4):
+        lens = _many(S, 900, 20 + seed)
+        at = np.minimum(np.concatenate([[0], np.cumsum(lens)]) + 5 * seed, total)
+        cu.copy_(torch.tensor(at, dtype=torch.int32))
+        O.zero_()
+        graph.replay()
+        got = O.clone()
+        want = torch.zeros_like(Q)
+        run(O=want)
+        assert torch.equal(got, want), seed
+        assert bool((got[:, at[0]:at[-1]] != 0).any(-1).all())
+    with pytest.raises(cca.CCAError):
+        run(O=O, workspace=ws[:n - 1])
+    assert cca.cca_device_status() == cca.CCA_OK
