@@ -40,7 +40,7 @@
 // Stretches that share a pair are joined in shared memory within a CTA, and
 // across CTAs by the last one that arrives at the pair (a ticket), always in
 // the order of the list: results do not depend on the order of arrival.
-// What is left beside the streaming is latency: of 31 us for 16 rows of up
+// What is left beside the streaming is latency: of 32 us for 16 rows of up
 // to 32K tokens (101 MB), 2 are for the list, 5 until the first tile, 2 for
 // each join.  (Smaller stretches handed out as CTAs get done: 190 us instead
 // of 130 for the 8 rows; a stretch's begin and end take 8 us.)
@@ -196,9 +196,9 @@ constexpr int kCore = 1 << 12, kNewest = 1 << 13, kFirst = 1 << 14, kEnds = 1 <<
 constexpr float kCoreUp = 15.f;
 
 // What a pair costs a warp beside its tiles (queries, output, page numbers),
-// and what a pooling does, in tiles: by the timeline of a batch of 64 rows of
+// and what a pooling does, in tiles: by the timeline of one batch, 64 rows of
 // 1 to 16K tokens, where CTAs with many short rows took twice as long as the
-// others without (72 us instead of 58).
+// others without (an earlier form of the kernel took 72 us instead of 58).
 constexpr int kPairTiles = 3, kPoolTiles = 4;
 
 // WIDE: 9 to 16 query heads for a key/value head; STEP: cca_paged_step.
@@ -1100,8 +1100,9 @@ cudaError_t launch_paged_decode(const cca_paged_cache &c, int layer, const void 
     const std::true_type wide{};
     const std::false_type narrow{};
     // 12 warps, as many as 168 registers allow, or 8 where more than 8 heads
-    // or the room ask for it (8 with a ring of 3: the 8 rows above in 135 us
-    // instead of 133).
+    // or the room ask for it.  (8 with a ring of 3, everywhere: the 8 rows
+    // above in 122 to 125 us instead of 124, 64 rows of 1 to 16K tokens with
+    // 8 key/value heads in 43 instead of 50.)
     if (c.d == 128) {
         if (r > 8) return run(d128, n8, n2, wide);
         if (fits(12, 2)) return run(d128, n12, n2, narrow);

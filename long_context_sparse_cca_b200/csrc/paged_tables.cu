@@ -483,8 +483,10 @@ __global__ void __launch_bounds__(kThreads) fork_pages_kernel(ForkView f)
 }
 
 // Both steps for a small batch, in one cluster: a warp for each row, then a
-// block for each pool.  8 rows with the copies and a reserve take 19 us
-// instead of 21; beyond two rows a warp, blocks of their own are faster.
+// block for each pool.  One launch less is 2 us of host time (6.9 instead of
+// 9.0 for a fork); on the GPU it gains nothing (8 rows with the copies and a
+// reserve: 18.6 us in a graph, 18.7 with blocks of their own; 256 rows: 18.8
+// and 15.7), and beyond two rows a warp it loses more (512 rows: 27.7 and 21.1).
 constexpr int kForkBlocks = 8, kForkRows = 2 * kForkBlocks * kThreads / 32;
 
 __global__ void __cluster_dims__(kForkBlocks, 1, 1) __launch_bounds__(kThreads)
