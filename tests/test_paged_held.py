@@ -244,3 +244,71 @@ def test_rows_that_ask_for_nothing_stay_what_they_were(built):
     assert cca.lib().cca_paged_reserve(r.c.struct, P(n.data_ptr()), 0, None) == cca.CCA_OK
     assert step() == [True, False]
     assert cca.cca_device_status() == cca.CCA_OK
+
+
+@pytest.mark.gpu
+def test_histories_under_random_calls(built):
+    """Prompts, steps, forks and compaction in small pools, in any order:
+    every row's keys are those that it was granted."""
+    assert sum(_random_calls(seed) for seed in range(8)) > 20
+
+
+def _random_calls(seed):
+    """Returns how many steps were refused."""
+    import random
+
+    import torch
+    rng = random.Random(seed)
+    B, g, w, page = rng.choice([3, 8]), 4, rng.choice([0, 10, 40]), 16
+    c = cca.PagedCache(B, 2, 1, D, g, w, page, rng.choice([4, 9]), rng.choice([8, 14]), max_len=160)
+    hist = [[] for _ in range(B)]
+    refused = 0
+
+    def check(what):
+        table, n = c.raw_table.cpu().numpy(), c.lens.tolist()
+        k = c.k_raw[0, :, 0].float().cpu().numpy()
+        for b in range(B):
+            assert n[b] == len(hist[b]), (what, b)
+            lo = max(n[b] - 1 - w, 0) // g * g
+            got = np.array([k[table[b, t // page], t % page] for t in range(lo, n[b])])
+            assert got.size == 0 or (got == np.array(hist[b][lo:])[:, None]).all(), (what, b)
+
+    for turn in range(120):
+        what = rng.choice("ssssspfc")
+        before = c.lens.tolist()
+        if what == "s":
+            cca.cca_paged_reserve(c, 1)
+            x = [rng.randrange(256) for _ in range(B)]
+            k = torch.tensor(x, device="cuda")[:, None, None].expand(B, 1, D).bfloat16()
+            q = torch.ones((B, 2, D), dtype=torch.bfloat16, device="cuda")
+            o = cca.cca_paged_step(c, q, k.contiguous(), k.contiguous())
+            for b, (a, z) in enumerate(zip(before, c.lens.tolist())):
+                if z > a:
+                    hist[b].append(x[b])
+                else:
+                    refused += a > 0
+                    assert bool((o[b] == 0).all())
+        elif what == "p":
+            n = [0 if a or rng.random() < 0.5 else rng.randint(1, 60) for a in before]
+            cca.cca_paged_reserve(c, torch.tensor(n, device="cuda"))
+            rows = [b for b, z in enumerate(c.lens.tolist()) if z and not before[b]]
+            if rows:
+                x = [[rng.randrange(256) for _ in range(n[b])] for b in rows]
+                flat = torch.tensor(sum(x, []), device="cuda")
+                K = flat[None, :, None].expand(1, -1, D).bfloat16().contiguous()
+                cu = torch.tensor([0, *np.cumsum([len(y) for y in x])], dtype=torch.int32,
+                                  device="cuda")
+                core = cca.cca_pool_packed(K.expand(2, -1, -1).contiguous(), K, K, cu, g)
+                cca.cca_paged_fill(c, K, K, *core, cu,
+                                   torch.tensor(rows, dtype=torch.int32, device="cuda"))
+                for b, y in zip(rows, x):
+                    hist[b] = y
+        elif what == "f":
+            parent = [rng.choice([b, b, b, rng.randint(-1, B - 1)]) for b in range(B)]
+            cca.cca_paged_fork(c, torch.tensor(parent, dtype=torch.int32, device="cuda"))
+            hist = [list(hist[p]) if p >= 0 and z else [] for p, z in zip(parent, c.lens.tolist())]
+        else:
+            cca.cca_paged_compact(c)
+        assert cca.cca_device_status() in (cca.CCA_OK, cca.CCA_ERR_CAPACITY), (turn, what)
+        check((turn, what))
+    return refused
