@@ -31,11 +31,10 @@
 // P_hi + P_lo up to 2^-17 (raw rows of more than 8 query heads: 2^-16, see
 // split2); for up to 8 query heads P_lo takes the fragment rows that are free,
 // and costs nothing.  An infinite value gives an infinite output, as with one
-// number, and not NaN.  fp16 has no numbers below 2^-24, so
-// core tiles hold weights relative to 2^-15 of the largest one (up to 2^15
-// then): one of 2^-n of the largest is off by 2^-17 of itself down to n = 23,
-// and by 2^-40 of the largest below.  Scores, running maximum and sum, and
-// outputs are fp32.
+// number, and not NaN.  fp16 has no numbers below 2^-24, so core tiles hold
+// weights relative to 2^-15 of the largest one (up to 2^15 then): one of 2^-n
+// of the largest is off by 2^-17 of itself down to n = 23, and by 2^-40 of the
+// largest below.  Scores, running maximum and sum, and outputs are fp32.
 //
 // Stretches that share a pair are joined in shared memory within a CTA, and
 // across CTAs by the last one that arrives at the pair (a ticket), always in

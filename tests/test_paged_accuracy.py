@@ -5,7 +5,8 @@ The bound.  With q in {-1, 0, 1} and keys that are multiples of 1/4 all scores
 are exact, so that against fp64 on the cache's own rows an output is off by
 at most e * sum_j w_j |v_j| + 2^-40 * sum_core |v_j|, w the softmax, e the
 sum of
-  2^-16          the weights' two numbers (8 bits each at least),
+  2^-16 + 2^-20  the weights' two numbers (8 bits each at least; for more
+                 than 8 query heads the second one has 2^-20 added),
   2^-21          ex2.approx, 2^-22 for the weights and for their sum,
   s * 2^-22      scaling the scores, at most s (log2 units), and subtracting
                  the maximum, for the weights and for their sum,
@@ -58,7 +59,7 @@ def _reference(c, q, b):
 def _off(got, ref):
     """How many times the bound an output is off."""
     o, size, core, s, n = ref
-    e = 2.0 ** -16 + 2.0 ** -21 + s * 2.0 ** -22 + n * 2.0 ** -22
+    e = 2.0 ** -16 + 2.0 ** -20 + 2.0 ** -21 + s * 2.0 ** -22 + n * 2.0 ** -22
     return float(((got.to(F64) - o).abs() / (e * size + 2.0 ** -40 * core + 1e-300)).max())
 
 
@@ -106,8 +107,8 @@ def _emulated(c, q, b, split, up):
     """Row b with the weights in one or two numbers of their tiles' types,
     core ones relative to 2^-up of the largest."""
     (kc, vc), (kr, vr) = _seen(c, b)
-    x = [q[b].to(F64).view(c.Hkv, -1, c.d) @ k.to(F64).transpose(1, 2) / math.sqrt(c.d) / math.log(2)
-         for k in (kc, kr)]
+    x = [q[b].to(F64).view(c.Hkv, -1, c.d) @ k.to(F64).transpose(1, 2) /
+         (math.sqrt(c.d) * math.log(2)) for k in (kc, kr)]
     top = torch.cat(x, -1).amax(-1, keepdim=True)
     num, den = 0.0, 0.0
     for s, v, dtype, u in ((x[0], vc, F16, up), (x[1], vr, BF, 0)):

@@ -203,10 +203,9 @@ def test_further_prompt_fills_the_whole_row_again(built, more):
     Q, K, V = (to_cuda(x) for x in h)
     cu, row = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, n], [0]))
     # not the new tokens alone: they are not as long as the row
-    cca.cca_paged_fill(r.c, K[:, :more], V[:, :more],
-                       *cca.cca_pool_packed(Q[:, :more], K[:, :more], V[:, :more],
-                                            cu - torch.tensor([0, n - more], device="cuda").int(), G),
-                       cu - torch.tensor([0, n - more], device="cuda").int(), row)
+    part = torch.tensor([0, more], dtype=torch.int32, device="cuda")
+    x = [t[:, :more] for t in (Q, K, V)]
+    cca.cca_paged_fill(r.c, *x[1:], *cca.cca_pool_packed(*x, part, G), part, row)
     assert cca.cca_device_status() == cca.CCA_ERR_PAGE
     cca.cca_paged_fill(r.c, K, V, *cca.cca_pool_packed(Q, K, V, cu, G), cu, row)
     assert cca.cca_device_status() == cca.CCA_OK
@@ -312,3 +311,21 @@ def _random_calls(seed):
         assert cca.cca_device_status() in (cca.CCA_OK, cca.CCA_ERR_CAPACITY), (turn, what)
         check((turn, what))
     return refused
+
+
+@pytest.mark.gpu
+def test_notes_are_in_the_workspace_of_the_call(built):
+    """A refusal noted in one workspace holds the row for steps with that one."""
+    import torch
+    r = Loop(2, [32, 20], 12, 2 + 2, layers=1)
+    ws = torch.zeros_like(r.c.workspace)
+    q, k, v = (to_cuda(synth.random_bf16((2, h, D), 20 + h)) for h in (HQ, HKV, HKV))
+    cca.cca_paged_reserve(r.c, 1, workspace=ws)  # row 0 has no page for token 32
+    assert cca.cca_device_status() == cca.CCA_ERR_CAPACITY
+    keep = r.c.k_raw.clone()
+    o = cca.cca_paged_step(r.c, q, k, v, workspace=ws)
+    assert bool((o[0] == 0).all()) and not bool((o[1] == 0).all())
+    row = r.c.raw_table[0][r.c.raw_table[0] >= 0].long()
+    assert torch.equal(r.c.k_raw[:, row], keep[:, row])
+    assert not bool((cca.cca_paged_step(r.c, q, k, v)[0] == 0).all())
+    assert cca.cca_device_status() == cca.CCA_OK
